@@ -36,6 +36,9 @@ VARIANTS = {"megakernel": MK_MEGAKERNEL, "multikernel": MK_MULTIKERNEL,
 MK_FAULT_NONE = 0
 MK_FAULT_UNREACHABLE_WAIT = 1
 MK_TRACE_WORDS = 12  # uint64 words per (op, warp) record of mk_set_trace
+MK_F32 = 0   # element types of the paged operators
+MK_BF16 = 1
+MK_E4M3 = 2
 MK_SAMPLE_PHASES = 12  # phase stamps of mk_sample_top_p_phases
 MK_STATIC_SCRATCH_BYTES = 32 << 20  # the fixed working array of mk_decode_step_static
 
@@ -64,6 +67,16 @@ class mk_weights(ctypes.Structure):
 
 class mk_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class mk_paged_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page_size", "max_pages", "n_kv_heads", "head_dim", "dtype")]
+
+
+class mk_strides(ctypes.Structure):
+    _fields_ = [("seq", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 class mk_stats(ctypes.Structure):
@@ -96,6 +109,7 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is missing: build it with decode_megakernel_06_b200/build.py")
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64
+    kvp = ctypes.POINTER(mk_paged_kv)
     sig = {
         "mk_create": (i32, [ctypes.POINTER(mk_model_desc), ctypes.POINTER(mk_weights), ctypes.POINTER(vp)]),
         "mk_decode_step": (i32, [vp, vp, vp, i32, i32, mk_kv_cache, vp, vp, vp]),
@@ -109,6 +123,14 @@ def lib():
                                         ctypes.c_float, vp, vp, vp]),
         "mk_decode_steps_sample": (i32, [vp, vp, vp, i32, i32, mk_kv_cache, vp, ctypes.c_float,
                                          ctypes.c_float, vp, vp, vp]),
+        "mk_kv_append": (i32, [kvp, vp, mk_strides, vp, mk_strides, i32, vp, vp, i32, i32, vp, i32, vp]),
+        "mk_kv_gather": (i32, [kvp, vp, vp, i32, i32, vp, mk_strides, vp, mk_strides, i32, vp]),
+        "mk_paged_attention_workspace": (u64, []),
+        "mk_paged_attention": (i32, [kvp, vp, mk_strides, i32, i32, vp, vp, i32, i32, ctypes.c_float, vp, i32, vp,
+                                     vp, u64, vp]),
+        "mk_verify_sample_workspace": (u64, [i32, i32]),
+        "mk_verify_sample": (i32, [vp, vp, vp, i32, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, u64,
+                                   vp]),
         "mk_get_device_status": (i32, [vp, vp]),
         "mk_last_device_error_op": (i32, [vp]),
         "mk_last_error": (ctypes.c_char_p, []),
@@ -222,6 +244,42 @@ def mk_decode_steps_sample(h, tokens: int, positions: int, B: int, n_steps: int,
                                         uniforms, out_tokens, stream)
 
 
+def mk_kv_append(kv: mk_paged_kv, k: int, ks: mk_strides, v: int, vs: mk_strides, in_dtype: int, positions: int,
+                 counts: Optional[int], B: int, T: int, rope: Optional[int], rope_len: int, stream: int) -> int:
+    """New rows into the pages of a cache (see include/mk.h)."""
+    return lib().mk_kv_append(ctypes.byref(kv), k, ks, v, vs, in_dtype, positions, counts, B, T, rope, rope_len, stream)
+
+
+def mk_kv_gather(kv: mk_paged_kv, starts: int, counts: Optional[int], B: int, T: int, k: int, ks: mk_strides, v: int,
+                 vs: mk_strides, out_dtype: int, stream: int) -> int:
+    """Positions of a paged cache read back (see include/mk.h)."""
+    return lib().mk_kv_gather(ctypes.byref(kv), starts, counts, B, T, k, ks, v, vs, out_dtype, stream)
+
+
+def mk_paged_attention_workspace() -> int:
+    return lib().mk_paged_attention_workspace()
+
+
+def mk_paged_attention(kv: mk_paged_kv, q: int, qs: mk_strides, dtype: int, n_q_heads: int, positions: int,
+                       counts: Optional[int], B: int, T: int, scale: float, rope: Optional[int], rope_len: int,
+                       out: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Attention of the newest rows over the pages (see include/mk.h)."""
+    return lib().mk_paged_attention(ctypes.byref(kv), q, qs, dtype, n_q_heads, positions, counts, B, T, scale, rope,
+                                    rope_len, out, workspace, workspace_bytes, stream)
+
+
+def mk_verify_sample_workspace(B: int, T: int) -> int:
+    return lib().mk_verify_sample_workspace(B, T)
+
+
+def mk_verify_sample(logits: int, draft_logits: Optional[int], tokens: int, B: int, T: int, vocab: int,
+                     temperature: float, top_p: float, uniforms: Optional[int], out_tokens: int, out_accepted: int,
+                     workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Acceptance of drafts by the target's probabilities (see include/mk.h)."""
+    return lib().mk_verify_sample(logits, draft_logits, tokens, B, T, vocab, temperature, top_p, uniforms, out_tokens,
+                                  out_accepted, workspace, workspace_bytes, stream)
+
+
 def _need(t, dtype, min_numel: int, name: str, device=None, dims: Optional[int] = None):
     """Check a tensor handed to a kernel by its data pointer: dtype, a
     contiguous layout with at least ``min_numel`` elements, optionally the
@@ -272,6 +330,183 @@ def sample_top_p_phases(logits, temperature: float, top_p: float, uniforms, out_
     s = stream if stream is not None else torch.cuda.current_stream()
     return mk_sample_top_p_phases(logits.data_ptr(), rows, vocab, temperature, top_p, _ptr(uniforms),
                                   out_tokens.data_ptr(), stamps.data_ptr(), s.cuda_stream)
+
+
+def _stream_of(device, stream) -> int:
+    """The CUDA stream of a call on ``device``: the given one, which has to be
+    that device's, or its current one."""
+    import torch
+
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"stream: on {s.device}, expected {device}")
+    return s.cuda_stream
+
+
+class PagedKV:
+    """One layer's paged cache over torch tensors: ``k`` and ``v`` are bf16 or
+    float8_e4m3fn [n_pages, n_kv_heads, page_size, head_dim], ``page_table`` is
+    int32 [B, max_pages] for the B sequences of a call, and an 8-bit cache has
+    fp32 scales [n_pages, n_kv_heads, page_size].  All contiguous, on one CUDA
+    device (ValueError otherwise).  The tensors are kept, not copied; the
+    operators are those of include/mk.h and return its status codes."""
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        import torch
+
+        kinds = {torch.bfloat16: MK_BF16, torch.float8_e4m3fn: MK_E4M3}
+        if k.dtype not in kinds:
+            raise ValueError(f"k: dtype {k.dtype}, expected bfloat16 or float8_e4m3fn")
+        _need(k, k.dtype, 1, "k", dims=4)
+        self.device = k.device
+        _need(v, k.dtype, 1, "v", self.device, dims=4)
+        if v.shape != k.shape:
+            raise ValueError(f"v: shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+        _need(page_table, torch.int32, 1, "page_table", self.device, dims=2)
+        n_pages, heads, page, hd = k.shape
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t is not None) != (k.dtype == torch.float8_e4m3fn):
+                raise ValueError(f"{name}: given for an 8-bit cache, and only for one")
+            if t is not None:
+                _need(t, torch.float32, 1, name, self.device, dims=3)
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(k.shape[:3])}")
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.desc = mk_paged_kv(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(),
+                                n_pages, page, page_table.shape[1], heads, hd, kinds[k.dtype])
+
+    def _rows(self, t, name: str, heads: Optional[int], like=None, written: bool = False):
+        """Checks a [B, T, heads, head_dim] operand (fp32 or bf16, any strides but a
+        contiguous head_dim); returns (B, T, heads), its strides and its type."""
+        import torch
+
+        kinds = {torch.float32: MK_F32, torch.bfloat16: MK_BF16}
+        if t.dtype not in kinds:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected float32 or bfloat16")
+        if t.dim() != 4 or t.shape[3] != self.desc.head_dim or (heads is not None and t.shape[2] != heads):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [B, T, "
+                             f"{'heads' if heads is None else heads}, {self.desc.head_dim}]")
+        if t.shape[0] != self.page_table.shape[0]:
+            raise ValueError(f"{name}: {t.shape[0]} sequences, the page table has {self.page_table.shape[0]}")
+        if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(like.shape)} {like.dtype}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}: the head dimension must be contiguous")
+        if written and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+            raise ValueError(f"{name}: written rows must not share memory")
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        return t.shape[:3], mk_strides(t.stride(0), t.stride(1), t.stride(2)), kinds[t.dtype]
+
+    def _sequences(self, B: int, positions, counts, rope):
+        """Checks the per-sequence operands; returns rope's number of positions."""
+        import torch
+
+        _need(positions, torch.int32, B, "positions", self.device)
+        if counts is not None:
+            _need(counts, torch.int32, B, "counts", self.device)
+        if rope is None:
+            return 0
+        _need(rope, torch.float32, 1, "rope", self.device, dims=3)
+        if tuple(rope.shape[1:]) != (self.desc.head_dim // 2, 2):
+            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, {self.desc.head_dim // 2}, 2]")
+        return rope.shape[0]
+
+    def append(self, k, v, positions, counts=None, rope=None, stream=None) -> int:
+        """mk_kv_append: rows k, v [B, T, n_kv_heads, head_dim] at positions[b] + t
+        (rows t >= counts[b] are not written); with rope, k is rotated first."""
+        import torch
+
+        (B, T, _), ks, kind = self._rows(k, "k", self.desc.n_kv_heads)
+        _, vs, _ = self._rows(v, "v", self.desc.n_kv_heads, like=k)
+        n = self._sequences(B, positions, counts, rope)
+        with torch.cuda.device(self.device):
+            return mk_kv_append(self.desc, k.data_ptr(), ks, v.data_ptr(), vs, kind, positions.data_ptr(),
+                                _ptr(counts), B, T, _ptr(rope), n, _stream_of(self.device, stream))
+
+    def gather(self, starts, out_k, out_v, counts=None, stream=None) -> int:
+        """mk_kv_gather: positions starts[b] + t into out_k, out_v
+        [B, T, n_kv_heads, head_dim] (any strides, e.g. a contiguous cache
+        [B, heads, capacity, head_dim] transposed)."""
+        import torch
+
+        (B, T, _), ks, kind = self._rows(out_k, "out_k", self.desc.n_kv_heads, written=True)
+        _, vs, _ = self._rows(out_v, "out_v", self.desc.n_kv_heads, like=out_k, written=True)
+        self._sequences(B, starts, counts, None)
+        with torch.cuda.device(self.device):
+            return mk_kv_gather(self.desc, starts.data_ptr(), _ptr(counts), B, T, out_k.data_ptr(), ks,
+                                out_v.data_ptr(), vs, kind, _stream_of(self.device, stream))
+
+    def attention(self, q, positions, out, workspace, counts=None, scale: Optional[float] = None, rope=None,
+                  stream=None) -> int:
+        """mk_paged_attention: rows q [B, T, n_q_heads, head_dim] at positions[b] + t
+        over the cache, into out (contiguous, like q); scale defaults to
+        1 / sqrt(head_dim).  ``workspace`` is paged_attention_workspace's."""
+        import torch
+
+        (B, T, heads), qs, kind = self._rows(q, "q", None)
+        _need(out, q.dtype, 1, "out", self.device, dims=4)
+        if out.shape != q.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+        n = self._sequences(B, positions, counts, rope)
+        _need(workspace, torch.uint8, 1, "workspace", self.device)
+        if scale is None:
+            scale = self.desc.head_dim ** -0.5
+        with torch.cuda.device(self.device):
+            return mk_paged_attention(self.desc, q.data_ptr(), qs, kind, heads, positions.data_ptr(), _ptr(counts),
+                                      B, T, scale, _ptr(rope), n, out.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel(), _stream_of(self.device, stream))
+
+
+def paged_attention_workspace(device):
+    """A workspace of PagedKV.attention on ``device`` (uint8, zeroed once).  Calls
+    that may overlap on the GPU need one each."""
+    import torch
+
+    with torch.cuda.device(device):
+        n = mk_paged_attention_workspace()
+        if n == 0:
+            raise MkError(MK_ERR_CUDA, mk_last_error())
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def verify_sample_workspace(B: int, T: int, vocab: int, device):
+    """A workspace of verify_sample for blocks of that size (uint8)."""
+    import torch
+
+    n = mk_verify_sample_workspace(B, T)
+    if n == 0 or vocab < 1:
+        raise ValueError(f"B, T and vocab must be >= 1 (got {B}, {T}, {vocab})")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def verify_sample(logits, tokens, temperature: float, top_p: float, uniforms, out_tokens, out_accepted, workspace,
+                  draft_logits=None, stream=None) -> int:
+    """Torch-tensor form of mk_verify_sample: logits fp32 [B, T, vocab], tokens int32
+    [B, T] (the last accepted token, then the drafts), draft_logits fp32
+    [B, T - 1, vocab] or None, uniforms fp64 [B, T] (None when temperature <= 0),
+    out_tokens int32 [B, T], out_accepted int32 [B], all contiguous on one CUDA
+    device (ValueError otherwise).  Returns the launch status code."""
+    import torch
+
+    _need(logits, torch.float32, 1, "logits", dims=3)
+    dev = logits.device
+    B, T, vocab = logits.shape
+    _need(tokens, torch.int32, B * T, "tokens", dev)
+    if draft_logits is not None:
+        _need(draft_logits, torch.float32, 0, "draft_logits", dev, dims=3)
+        if tuple(draft_logits.shape) != (B, T - 1, vocab):
+            raise ValueError(f"draft_logits: shape {tuple(draft_logits.shape)}, expected {(B, T - 1, vocab)}")
+    if uniforms is not None:
+        _need(uniforms, torch.float64, B * T, "uniforms", dev)
+    _need(out_tokens, torch.int32, B * T, "out_tokens", dev)
+    _need(out_accepted, torch.int32, B, "out_accepted", dev)
+    _need(workspace, torch.uint8, 1, "workspace", dev)
+    with torch.cuda.device(dev):
+        return mk_verify_sample(logits.data_ptr(), _ptr(draft_logits) if T > 1 else None, tokens.data_ptr(), B, T,
+                                vocab, temperature, top_p, _ptr(uniforms), out_tokens.data_ptr(),
+                                out_accepted.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                _stream_of(dev, stream))
 
 
 def hbm_read_probe(buf, form: int = 0, reps: int = 5, stream=None) -> float:

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libmk.so")
 # second time with the timeline trace compiled in.
 UNITS = [("mk_kernel.cu", "mk_kernel", []), ("mk_kernel.cu", "mk_kernel_trace", ["-DMK_TRACE=1"]),
          ("mk_api.cu", "mk_api", []), ("mk_wide.cu", "mk_wide", []), ("mk_sample.cu", "mk_sample", []),
-         ("mk_probe.cu", "mk_probe", [])]
+         ("mk_probe.cu", "mk_probe", []), ("mk_paged.cu", "mk_paged", []), ("mk_verify.cu", "mk_verify", [])]
 SOURCES = sorted({u[0] for u in UNITS})
 HEADERS = ["mk_internal.h", os.path.join("..", "..", "include", "mk.h")]
 

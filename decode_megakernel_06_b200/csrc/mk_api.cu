@@ -897,6 +897,158 @@ MK_API int mk_decode_step_sample(mk_handle *h, const int32_t *tokens, const int3
   return MK_OK;
 }
 
+// ---- paged cache ------------------------------------------------------------------
+static bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+static int check_paged_kv(const mk_paged_kv *kv) {
+  if (!kv) return fail(MK_ERR_ARG, "kv is NULL");
+  if (kv->dtype != MK_BF16 && kv->dtype != MK_E4M3)
+    return fail(MK_ERR_UNSUPPORTED, "a paged cache holds MK_BF16 or MK_E4M3 (got dtype %d)", kv->dtype);
+  if (!kv->k || !kv->v || !kv->page_table) return fail(MK_ERR_ARG, "kv.k, kv.v and kv.page_table are required");
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return fail(MK_ERR_ARG, "kv.k and kv.v must be 16-byte aligned");
+  if (!aligned(kv->page_table, 4)) return fail(MK_ERR_ARG, "kv.page_table must be 4-byte aligned");
+  if (kv->dtype == MK_E4M3 && (!kv->k_scale || !kv->v_scale || !aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)))
+    return fail(MK_ERR_ARG, "an MK_E4M3 cache needs kv.k_scale and kv.v_scale, 4-byte aligned");
+  if (kv->dtype == MK_BF16 && (kv->k_scale || kv->v_scale))
+    return fail(MK_ERR_ARG, "an MK_BF16 cache takes no scales (kv.k_scale and kv.v_scale must be NULL)");
+  if (kv->n_pages < 1 || kv->page_size < 1 || kv->max_pages < 1 || kv->n_kv_heads < 1)
+    return fail(MK_ERR_ARG, "n_pages, page_size, max_pages and n_kv_heads must be >= 1");
+  if (kv->head_dim != 64 && kv->head_dim != 128)
+    return fail(MK_ERR_UNSUPPORTED, "head_dim %d unsupported (64 or 128)", kv->head_dim);
+  const long long row = (long long)kv->n_kv_heads * kv->page_size;
+  if (row >= (1ll << 31) || row * kv->n_pages >= (1ll << 31) || (long long)kv->max_pages * kv->page_size >= (1ll << 31))
+    return fail(MK_ERR_UNSUPPORTED, "the pool and a page table's row hold fewer than 2^31 positions");
+  return MK_OK;
+}
+
+static int check_rows(const mk_paged_kv *kv, int32_t B, int32_t T, int32_t dtype, const int32_t *positions,
+                      const float *rope, int32_t rope_len) {
+  if (B < 1 || T < 1) return fail(MK_ERR_ARG, "B and T must be >= 1 (got %d, %d)", B, T);
+  if (dtype != MK_F32 && dtype != MK_BF16)
+    return fail(MK_ERR_UNSUPPORTED, "rows are MK_F32 or MK_BF16 (got dtype %d)", dtype);
+  if (!positions) return fail(MK_ERR_ARG, "the sequences' positions are required");
+  if (rope && (rope_len < 1 || !aligned(rope, 8)))
+    return fail(MK_ERR_ARG, "rope needs rope_len >= 1 and 8-byte alignment");
+  if ((long long)T * kv->n_kv_heads >= (1ll << 30))
+    return fail(MK_ERR_UNSUPPORTED, "T * n_kv_heads must be below 2^30");
+  return MK_OK;
+}
+
+// Rows of head_dim elements that start on 16-byte boundaries whatever the index.
+static int vec_ok(const void *p, const mk_strides &s, int32_t dtype) {
+  const long long n = dtype == MK_F32 ? 4 : 8;
+  return aligned(p, 16) && s.seq % n == 0 && s.token % n == 0 && s.head % n == 0;
+}
+
+static int check_operand(const void *p, int32_t dtype, const char *name) {
+  if (!p) return fail(MK_ERR_ARG, "%s is NULL", name);
+  if (!aligned(p, dtype == MK_F32 ? 4 : 2)) return fail(MK_ERR_ARG, "%s is not aligned to its elements", name);
+  return MK_OK;
+}
+
+MK_API int mk_kv_append(const mk_paged_kv *kv, const void *k, mk_strides ks, const void *v, mk_strides vs,
+                        int32_t in_dtype, const int32_t *positions, const int32_t *counts, int32_t B, int32_t T,
+                        const float *rope, int32_t rope_len, void *stream) {
+  int rc = check_paged_kv(kv);
+  if (!rc) rc = check_rows(kv, B, T, in_dtype, positions, rope, rope_len);
+  if (!rc) rc = check_operand(k, in_dtype, "k");
+  if (!rc) rc = check_operand(v, in_dtype, "v");
+  if (rc) return rc;
+  KvAppend a{};
+  a.kv = *kv;
+  a.k = k; a.v = v; a.ks = ks; a.vs = vs;
+  a.positions = positions; a.counts = counts;
+  a.B = B; a.T = T;
+  a.rope = reinterpret_cast<const float2 *>(rope); a.rope_len = rope_len;
+  a.vec = vec_ok(k, ks, in_dtype) && vec_ok(v, vs, in_dtype);
+  CUDA_TRY(launch_kv_append(a, in_dtype, static_cast<cudaStream_t>(stream)));
+  return MK_OK;
+}
+
+MK_API int mk_kv_gather(const mk_paged_kv *kv, const int32_t *starts, const int32_t *counts, int32_t B, int32_t T,
+                        void *k, mk_strides ks, void *v, mk_strides vs, int32_t out_dtype, void *stream) {
+  int rc = check_paged_kv(kv);
+  if (!rc) rc = check_rows(kv, B, T, out_dtype, starts, nullptr, 0);
+  if (!rc) rc = check_operand(k, out_dtype, "k");
+  if (!rc) rc = check_operand(v, out_dtype, "v");
+  if (rc) return rc;
+  KvGather a{};
+  a.kv = *kv;
+  a.starts = starts; a.counts = counts;
+  a.B = B; a.T = T;
+  a.k = k; a.v = v; a.ks = ks; a.vs = vs;
+  a.vec = vec_ok(k, ks, out_dtype) && vec_ok(v, vs, out_dtype);
+  CUDA_TRY(launch_kv_gather(a, out_dtype, static_cast<cudaStream_t>(stream)));
+  return MK_OK;
+}
+
+static int current_sm_count(int *n_sm) {
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  CUDA_TRY(cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, dev));
+  return MK_OK;
+}
+
+MK_API uint64_t mk_paged_attention_workspace(void) {
+  int n_sm = 0;
+  return current_sm_count(&n_sm) ? 0 : paged_attention_workspace(n_sm);
+}
+
+MK_API int mk_paged_attention(const mk_paged_kv *kv, const void *q, mk_strides qs, int32_t dtype, int32_t n_q_heads,
+                              const int32_t *positions, const int32_t *counts, int32_t B, int32_t T, float scale,
+                              const float *rope, int32_t rope_len, void *out, void *workspace,
+                              uint64_t workspace_bytes, void *stream) {
+  int rc = check_paged_kv(kv);
+  if (!rc) rc = check_rows(kv, B, T, dtype, positions, rope, rope_len);
+  if (!rc) rc = check_operand(q, dtype, "q");
+  if (!rc) rc = check_operand(out, dtype, "out");
+  if (rc) return rc;
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads)
+    return fail(MK_ERR_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
+  if ((long long)T * n_q_heads >= (1ll << 30)) return fail(MK_ERR_UNSUPPORTED, "T * n_q_heads must be below 2^30");
+  if (!std::isfinite(scale)) return fail(MK_ERR_ARG, "scale must be finite");
+  if (!workspace || !aligned(workspace, 16)) return fail(MK_ERR_ARG, "workspace must be given, 16-byte aligned");
+  int n_sm = 0;
+  rc = current_sm_count(&n_sm);
+  if (rc) return rc;
+  if (workspace_bytes < paged_attention_workspace(n_sm))
+    return fail(MK_ERR_CAPACITY, "workspace of %llu bytes, %llu needed", (unsigned long long)workspace_bytes,
+                (unsigned long long)paged_attention_workspace(n_sm));
+  PagedAttn a{};
+  a.kv = *kv;
+  a.q = q; a.qs = qs; a.Hq = n_q_heads;
+  a.positions = positions; a.counts = counts;
+  a.B = B; a.T = T; a.scale = scale;
+  a.rope = reinterpret_cast<const float2 *>(rope); a.rope_len = rope_len;
+  a.out = out;
+  CUDA_TRY(launch_paged_attention(a, dtype, workspace, static_cast<cudaStream_t>(stream)));
+  return MK_OK;
+}
+
+MK_API uint64_t mk_verify_sample_workspace(int32_t B, int32_t T) {
+  return B < 1 || T < 1 ? 0 : verify_sample_workspace(B, T);
+}
+
+MK_API int mk_verify_sample(const float *logits, const float *draft_logits, const int32_t *tokens, int32_t B,
+                            int32_t T, int32_t vocab, float temperature, float top_p, const double *uniforms,
+                            int32_t *out_tokens, int32_t *out_accepted, void *workspace, uint64_t workspace_bytes,
+                            void *stream) {
+  if (B < 1 || T < 1) return fail(MK_ERR_ARG, "B and T must be >= 1 (got %d, %d)", B, T);
+  if ((long long)B * T >= (1ll << 24)) return fail(MK_ERR_UNSUPPORTED, "B * T must be below 2^24");
+  int rc = check_sample_args(logits, B * T, vocab, temperature, top_p, uniforms, out_tokens);
+  if (rc) return rc;
+  if (!tokens || !out_accepted) return fail(MK_ERR_ARG, "tokens and out_accepted must not be NULL");
+  if (tokens == out_tokens) return fail(MK_ERR_ARG, "out_tokens must not overlap tokens");
+  if (!workspace || !aligned(workspace, 16)) return fail(MK_ERR_ARG, "workspace must be given, 16-byte aligned");
+  if (workspace_bytes < verify_sample_workspace(B, T))
+    return fail(MK_ERR_CAPACITY, "workspace of %llu bytes, %llu needed", (unsigned long long)workspace_bytes,
+                (unsigned long long)verify_sample_workspace(B, T));
+  const VerifySample v{logits, draft_logits, tokens, B, T, vocab, temperature, top_p, uniforms, out_tokens,
+                       out_accepted, workspace};
+  CUDA_TRY(launch_verify_sample(v, static_cast<cudaStream_t>(stream)));
+  return MK_OK;
+}
+
 // positions of step s of a sampled loop: out[s][b] = positions[b] + s
 __global__ void sp_positions(const int32_t *positions, int B, int n_steps, int32_t *out) {
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < B * n_steps; i += gridDim.x * blockDim.x)

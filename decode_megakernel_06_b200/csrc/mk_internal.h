@@ -246,4 +246,54 @@ cudaError_t launch_top_p(const float *logits, int rows, int vocab, float tempera
 size_t probe_sink_words(int n_sm);
 cudaError_t launch_read_probe(const void *buf, size_t bytes, int form, int n_sm, uint32_t *sink, cudaStream_t s);
 
+// ---- paged cache (mk_paged.cu) and draft verification (mk_verify.cu) -----------
+struct KvAppend {
+  mk_paged_kv kv;
+  const void *k, *v;
+  mk_strides ks, vs;
+  const int32_t *positions, *counts;
+  int B, T;
+  const float2 *rope;
+  int rope_len;
+  int vec;  // operands allow 16-byte accesses
+};
+cudaError_t launch_kv_append(const KvAppend &a, int in_dtype, cudaStream_t st);
+
+struct KvGather {
+  mk_paged_kv kv;
+  const int32_t *starts, *counts;
+  int B, T;
+  void *k, *v;
+  mk_strides ks, vs;
+  int vec;
+};
+cudaError_t launch_kv_gather(const KvGather &a, int out_dtype, cudaStream_t st);
+
+struct PagedAttn {
+  mk_paged_kv kv;
+  const void *q;
+  mk_strides qs;
+  int Hq;
+  const int32_t *positions, *counts;
+  int B, T;
+  float scale;
+  const float2 *rope;
+  int rope_len;
+  void *out;
+};
+size_t paged_attention_workspace(int n_sm);
+cudaError_t launch_paged_attention(const PagedAttn &a, int dtype, void *workspace, cudaStream_t st);
+
+struct VerifySample {
+  const float *logits, *draft_logits;
+  const int32_t *tokens;
+  int B, T, V;
+  float temperature, top_p;
+  const double *uniforms;
+  int32_t *out_tokens, *out_accepted;
+  void *workspace;
+};
+size_t verify_sample_workspace(int B, int T);
+cudaError_t launch_verify_sample(const VerifySample &a, cudaStream_t st);
+
 }  // namespace mk

@@ -318,6 +318,152 @@ MK_API int mk_decode_steps_sample(mk_handle *h, const int32_t *tokens, const int
                                   float temperature, float top_p, const double *uniforms,
                                   int32_t *out_tokens, void *stream);
 
+/* ---- paged key/value cache ----------------------------------------------------
+ * A cache in pages of page_size positions, shared by the sequences of a batch
+ * through a page table: position p of sequence b is slot p % page_size of page
+ * page_table[b][p / page_size].  Beside the contiguous bf16 cache of the decode
+ * step it holds sequences of very different lengths without reserving
+ * kv_capacity for each, and, as MK_E4M3, in half the bytes.
+ *
+ * Element types of the paged operators. */
+#define MK_F32 0
+#define MK_BF16 1
+#define MK_E4M3 2 /* 8-bit float (4 exponent, 3 mantissa bits, largest value 448) */
+
+/* One layer's cache.  Every pointer is a device pointer, 16-byte aligned (the
+ * scales and the table 4-byte), caller-owned; the pools and operands of a call do not
+ * overlap what it writes.
+ *   k, v     : [n_pages][n_kv_heads][page_size][head_dim] of `dtype` (MK_BF16 or
+ *              MK_E4M3); keys count as already rotated
+ *   k_scale, v_scale: MK_E4M3: fp32 [n_pages][n_kv_heads][page_size], one scale
+ *              per (position, head): the value held is code * scale.  MK_BF16: NULL
+ *   page_table: int32 [B][max_pages] for the B of the call.  An entry outside
+ *              [0, n_pages) is an unmapped page: its positions are not written,
+ *              read back as zeros and are not attended to
+ * Supported: head_dim 64 or 128; n_kv_heads >= 1; page_size >= 1; positions of a
+ * pool (n_pages * n_kv_heads * page_size) and of a table row (max_pages *
+ * page_size) below 2^31. */
+typedef struct mk_paged_kv {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t *page_table;
+  int32_t n_pages, page_size, max_pages;
+  int32_t n_kv_heads, head_dim, dtype;
+} mk_paged_kv;
+
+/* Strides of a [B][T][heads][head_dim] operand, in elements (head_dim is
+ * contiguous): the same call takes slices of a fused QKV row and the contiguous
+ * cache [B][heads][capacity][head_dim]. */
+typedef struct mk_strides {
+  int64_t seq, token, head;
+} mk_strides;
+
+/* Writes T new positions of B sequences into the pages: row t of sequence b at
+ * position positions[b] + t.
+ *   k, v       : device [B][T][n_kv_heads][head_dim] of in_dtype (MK_F32 or
+ *                MK_BF16), strides `ks` / `vs`
+ *   positions  : device int32 [B]
+ *   counts     : device int32 [B] or NULL: rows t >= counts[b] are not written
+ *                (a ragged batch); NULL writes all T
+ *   rope       : device fp32 [rope_len][head_dim / 2][2] (rope_len >= 1, 8-byte aligned),
+ *                (cos, sin) of each position's angles, or NULL.  With it k is rotated first (rotate-half:
+ *                i with i + head_dim / 2), in fp32; a row at or past rope_len is not written
+ *   MK_BF16    : each value is rounded to nearest even.
+ *   MK_E4M3    : per row of head_dim values x: scale = max(amax / 448, 2^-126),
+ *                code = round-to-nearest-even(x / scale); amax is over the finite values,
+ *                infinities become the largest code of their sign, NaN stays NaN.
+ * Rows at negative positions, past the table's end or on unmapped pages are not
+ * written; rows that two sequences map to one slot are the caller's race.
+ * Needs no workspace; one launch; asynchronous on `stream`.  Errors: MK_ERR_ARG,
+ * MK_ERR_UNSUPPORTED (head_dim, sizes past the limits), MK_ERR_CUDA. */
+MK_API int mk_kv_append(const mk_paged_kv *kv, const void *k, mk_strides ks, const void *v, mk_strides vs,
+                        int32_t in_dtype, const int32_t *positions, const int32_t *counts, int32_t B, int32_t T,
+                        const float *rope, int32_t rope_len, void *stream);
+
+/* Reads T positions of B sequences back: out[b][t][head] = the value held at
+ * position starts[b] + t (code * scale for MK_E4M3), in fp32 and rounded once to
+ * out_dtype (MK_F32 or MK_BF16).  Positions that are not mapped give zeros; rows
+ * t >= counts[b] are left as they were.  With the strides of the contiguous cache
+ * of mk_decode_step, a paged sequence moves into that cache.
+ * Arguments as mk_kv_append; one launch; asynchronous.  Errors: the same. */
+MK_API int mk_kv_gather(const mk_paged_kv *kv, const int32_t *starts, const int32_t *counts, int32_t B, int32_t T,
+                        void *k, mk_strides ks, void *v, mk_strides vs, int32_t out_dtype, void *stream);
+
+/* Bytes of the workspace of mk_paged_attention on the current device.  Zero it
+ * once; every call leaves its counters zero again.  Calls that share a
+ * workspace must not overlap on the GPU: order them on one stream, or give
+ * each stream (and each graph that may run beside another) its own.
+ * 0 when no device is available. */
+MK_API uint64_t mk_paged_attention_workspace(void);
+
+/* Attention of the T newest tokens of each of B sequences over the paged
+ * cache, their own positions included (append them first): for query head h
+ * (KV head h / (n_q_heads / n_kv_heads)) of row t of sequence b
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  j in 0 .. positions[b] + t,
+ * over the mapped positions.  A row that sees no position gives zeros.  Values
+ * behind a row's last position, and on unmapped pages, are never used, whatever
+ * they hold.
+ *   q          : device [B][T][n_q_heads][head_dim] of `dtype` (MK_F32 or MK_BF16),
+ *                strides `qs`
+ *   positions  : device int32 [B]: position of row 0; negative: rows at negative
+ *                positions see nothing
+ *   counts     : device int32 [B] or NULL: rows t >= counts[b] are neither read nor
+ *                written
+ *   scale      : finite, e.g. 1 / sqrt(head_dim)
+ *   rope       : as mk_kv_append, applied to q at its row's position; or NULL.  A row
+ *                at or past rope_len gives zeros
+ *   out        : device [B][T][n_q_heads][head_dim] of `dtype`, contiguous
+ *   workspace  : see mk_paged_attention_workspace; 16-byte aligned
+ * Scores, softmax statistics and sums are fp32.  The result does not depend on
+ * which block finishes first.  One launch; asynchronous.  Errors: MK_ERR_ARG,
+ * MK_ERR_UNSUPPORTED, MK_ERR_CAPACITY (workspace too small), MK_ERR_CUDA. */
+MK_API int mk_paged_attention(const mk_paged_kv *kv, const void *q, mk_strides qs, int32_t dtype, int32_t n_q_heads,
+                              const int32_t *positions, const int32_t *counts, int32_t B, int32_t T, float scale,
+                              const float *rope, int32_t rope_len, void *out, void *workspace,
+                              uint64_t workspace_bytes, void *stream);
+
+/* Bytes of the workspace of mk_verify_sample (no initial value needed; not
+ * shared between calls that may overlap). */
+MK_API uint64_t mk_verify_sample_workspace(int32_t B, int32_t T);
+
+/* Verification of drafted tokens by the target's probabilities: the sampled
+ * form of the acceptance of mk_verify_steps (speculative sampling: Leviathan et
+ * al. 2023, algorithm 1; Chen et al. 2023).  The tokens that come out are
+ * distributed as mk_sample_top_p's on the target's logits, whatever the drafts.
+ * Block b holds T rows: tokens[b][0] is the last accepted token, tokens[b][1 ..
+ * T-1] the drafts, and logits row t scores the token after row t.  With a_t the
+ * nucleus masses of logits row t under (temperature, top_p), exactly those of
+ * mk_sample_top_p, A_t their sum, and d_t, D_t those of draft_logits row t:
+ *   draft x = tokens[b][t + 1] is accepted if u_t * (d_t[x] * A_t) < a_t[x] * D_t
+ *   (in fp64, products in that order), u_t = uniforms[b][t], t = 0, 1, ..;
+ *   at the first draft that is not (row s), the token is drawn from the
+ *   residual masses max(0, rint(a_s * (2^46 / A_s)) - rint(d_s * (2^46 / D_s))), or
+ *   from a_s where they are all zero;
+ *   when every draft is accepted (s = T - 1), from a_s.
+ * The draw takes the first id, in id order, whose cumulative mass exceeds
+ * y = min(R - 1, floor(u * R)), R the masses' sum, u = uniforms[b][T - 1].
+ * draft_logits NULL means drafts that are certain (n-grams, a greedy draft): d is
+ * 1 at the draft: accepted if u_t * A_t < a_t[x], residual a_s without x.
+ * A draft outside [0, vocab) ends its block: the token there is drawn from a_s,
+ * so that blocks of one call may hold fewer drafts than T - 1.
+ * temperature <= 0: a draft is accepted if it is the row's argmax (lowest id on
+ * ties), and the token is the argmax; uniforms and draft_logits are not read.
+ *   logits      : device fp32 [B][T][vocab]: finite, or -inf for a banned token
+ *   draft_logits: device fp32 [B][T-1][vocab], the same; or NULL
+ *   tokens      : device int32 [B][T], the block the step scored
+ *   uniforms    : device fp64 [B][T] in [0, 1)
+ *   out_tokens  : device int32 [B][T]: accepted drafts, the drawn token, then -1
+ *                 (not overlapping tokens)
+ *   out_accepted: device int32 [B]: tokens given out (1 .. T)
+ *   workspace   : at least mk_verify_sample_workspace(B, T) bytes, 16-byte aligned
+ * B, T >= 1 (B * T < 2^24); vocab 1 .. 131072.  A row without a finite logit gives an
+ * unspecified token in [0, vocab).  Asynchronous.  Errors: MK_ERR_ARG,
+ * MK_ERR_UNSUPPORTED, MK_ERR_CAPACITY (workspace), MK_ERR_CUDA. */
+MK_API int mk_verify_sample(const float *logits, const float *draft_logits, const int32_t *tokens, int32_t B,
+                            int32_t T, int32_t vocab, float temperature, float top_p, const double *uniforms,
+                            int32_t *out_tokens, int32_t *out_accepted, void *workspace, uint64_t workspace_bytes,
+                            void *stream);
+
 /* The same step driven from HOST buffers: copies tokens [B*T] and positions
  * [B] to the device, runs the step, copies argmax [B*T] back to
  * out_argmax_host, and waits for the stream.  Logits stay on the device
