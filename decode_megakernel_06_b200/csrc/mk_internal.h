@@ -282,7 +282,7 @@ struct PagedAttn {
   void *out;
 };
 size_t paged_attention_workspace(int n_sm);
-cudaError_t launch_paged_attention(const PagedAttn &a, int dtype, void *workspace, cudaStream_t st);
+cudaError_t launch_paged_attention(const PagedAttn &a, int dtype, void *workspace, int n_sm, cudaStream_t st);
 
 struct VerifySample {
   const float *logits, *draft_logits;
