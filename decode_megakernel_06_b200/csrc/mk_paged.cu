@@ -310,7 +310,8 @@ struct AtShape {
   static constexpr int NP = sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int kQBytes = Geo<HD, E4M3>::KS * NQ * NT * 32 * 8;      // fragments of Q^T
   static constexpr int kStage = kRows * HD * 4;                             // rotated q, fp32
-  static constexpr int kMerge = kAtWarps * kRows * HD * 4;                  // the warps' sums
+  static constexpr int kLd = HD + 2;                                        // row stride of the warps' sums
+  static constexpr int kMerge = kAtWarps * kRows * kLd * 4;
   static constexpr int kSmem = kMerge > kQBytes + kStage ? kMerge : kQBytes + kStage;
   static constexpr int kBlocks = NT == 1 ? 3 : 2;                           // resident per SM
 };
@@ -321,8 +322,8 @@ struct AttnArgs {
   uint32_t magic, shift;     // p / page_size = (p * magic) >> shift for 0 <= p < 2^31
   int cap;                   // positions of a page table's row
   float qscale;              // scale * log2(e)
-  float *part;               // [2 * blocks][kRows][HD] sums, then [2 * blocks][kRows][2] (reference, sum of weights)
-  float *part_ml;
+  float *part;               // [2 * blocks][kRows][HD] sums
+  float2 *part_ml;           // [2 * blocks][kRows] (reference, sum of weights)
   uint32_t *count;           // [blocks] per item, then [2 * blocks] per group of the first level
 };
 
@@ -342,11 +343,11 @@ template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -433,10 +434,10 @@ __global__ void __launch_bounds__(kAtThreads, (AtShape<HD, TIO, E4M3, NT>::kBloc
 paged_attn(const __grid_constant__ AttnArgs p) {
   using S = AtShape<HD, TIO, E4M3, NT>;
   using X = Geo<HD, E4M3>;
-  constexpr int kRows = S::kRows, NQ = S::NQ, NP = S::NP, KS = X::KS, KW = X::KW, VW = X::VW;
+  constexpr int kRows = S::kRows, NQ = S::NQ, NP = S::NP, KS = X::KS, KW = X::KW, VW = X::VW, kLd = S::kLd;
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ long long s_scan[kAtWarps];
-  __shared__ long long s_at[2];
+  __shared__ long long s_at;
   __shared__ int s_b;
   __shared__ float s_f[kRows];                  // factor of a row's scores
   __shared__ int s_lim[kRows];                  // last position a row sees, -1: none
@@ -451,27 +452,9 @@ paged_attn(const __grid_constant__ AttnArgs p) {
   pdl_wait();
   pdl_launch();
 
-  // ---- this block's share of the units ------------------------------------------------
-  long long mine = 0;
-  for (int b = tid; b < a.B; b += kAtThreads) mine += seq_units(p, kRows, b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_scan[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kAtWarps; ++w) total += s_scan[w];
-  if (total == 0) return;
-  const long long nb = min(static_cast<long long>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
-  if (blockIdx.x >= nb) return;
-  const long long u0 = blockIdx.x * total / nb, u1 = (blockIdx.x + 1) * total / nb;
-  auto block_of = [&](long long u) { return static_cast<int>(((u + 1) * nb - 1) / total); };
-
-  // ---- the sequence that holds unit u0 -------------------------------------------------
-  long long base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
-    const int b = b0 + tid;
-    const long long n = b < a.B ? seq_units(p, kRows, b) : 0;
+  // ---- this block's share of the units, and the sequence that holds its first ------------
+  // inclusive sum of n over the block's threads, and over all of them
+  auto block_scan = [&](long long n, long long &all) {
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -480,21 +463,46 @@ paged_attn(const __grid_constant__ AttnArgs p) {
     }
     __syncthreads();
     if (lane == 31) s_scan[warp] = incl;
-    if (tid == 0) s_b = -1;
     __syncthreads();
-    long long before = base;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
-    if (n > 0 && before + incl - n <= u0 && u0 < before + incl) {
-      s_b = b;
-      s_at[0] = before + incl - n;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kAtWarps; ++w) {
+      if (w < warp) incl += s_scan[w];
+      all += s_scan[w];
+    }
+    return incl;
+  };
+  long long total = 0, n = 0, incl = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
+    long long all;
+    n = b0 + tid < a.B ? seq_units(p, kRows, b0 + tid) : 0;
+    incl = block_scan(n, all);
+    total += all;
+  }
+  if (total == 0) return;
+  const long long nb = min(static_cast<long long>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
+  if (blockIdx.x >= nb) return;
+  const long long u0 = blockIdx.x * total / nb, u1 = (blockIdx.x + 1) * total / nb;
+  auto block_of = [&](long long u) { return static_cast<int>(((u + 1) * nb - 1) / total); };
+  if (tid == 0) s_b = -1;
+  __syncthreads();
+  long long base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
+    if (a.B > kAtThreads) {  // else n and incl are still those of the only pass
+      long long all;
+      n = b0 + tid < a.B ? seq_units(p, kRows, b0 + tid) : 0;
+      incl = block_scan(n, all) + base;
+      base += all;
+    }
+    if (n > 0 && incl - n <= u0 && u0 < incl) {
+      s_b = b0 + tid;
+      s_at = incl - n;
     }
     __syncthreads();
     if (s_b >= 0) break;
-#pragma unroll
-    for (int w = 0; w < kAtWarps; ++w) base += s_scan[w];
   }
   int b = s_b, rg = 0, h = 0;
-  long long at = s_at[0];  // first unit of item (b, rg, h)
+  long long at = s_at;  // first unit of item (b, rg, h)
 
   for (long long u = u0; u < u1;) {
     // the item that holds unit u: row groups in order, each with all KV heads
@@ -516,56 +524,118 @@ paged_attn(const __grid_constant__ AttnArgs p) {
     const bool whole = seg0 == 0 && seg1 == cost;
     const int pos = a.positions[b], n_rows = seq_rows(a, b), r0 = rg * kRows;
 
+    // ---- loads of a unit, a whole one ahead of its products ------------------------------
+    const int32_t *table = a.kv.page_table + static_cast<long long>(b) * a.kv.max_pages;
+    const long long all_see = static_cast<long long>(pos) + r0 / p.G;  // last position that every row sees
+    // pool row of position 16 unit + lane % 16, or -1
+    auto row_at = [&](int unit) {
+      const int q = unit * kUnit + (lane & 15);
+      if (unit >= seg1 || q >= len) return -1;
+      const int e = static_cast<int>((static_cast<unsigned long long>(q) * p.magic) >> p.shift);
+      const int page = table[e];
+      if (page < 0 || page >= a.kv.n_pages) return -1;
+      return (page * a.kv.n_kv_heads + h) * a.kv.page_size + (q - e * a.kv.page_size);
+    };
+    uint32_t kw[2][KW], vw[4][VW];
+    float ksc = 0.f, vsc = 0.f;  // scales of position lane % 16
+    auto load_k = [&](int row) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int r = __shfl_sync(0xffffffffu, row, g + 8 * s);
+        const char *src = static_cast<const char *>(a.kv.k) + static_cast<long long>(r) * (HD * X::kBytes);
+#pragma unroll
+        for (int i = 0; i < KW / 4; ++i) {
+          const uint4 x = r >= 0 ? ld_cache(reinterpret_cast<const uint4 *>(src) + i * 4 + c) : make_uint4(0, 0, 0, 0);
+          kw[s][4 * i] = x.x; kw[s][4 * i + 1] = x.y; kw[s][4 * i + 2] = x.z; kw[s][4 * i + 3] = x.w;
+        }
+      }
+      if constexpr (E4M3) {
+        ksc = row >= 0 ? a.kv.k_scale[row] : 0.f;
+        vsc = row >= 0 ? a.kv.v_scale[row] : 0.f;
+      }
+    };
+    auto load_v = [&](int row) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int r = __shfl_sync(0xffffffffu, row, 2 * c + (s & 1) + 8 * (s >> 1));
+        const char *src = static_cast<const char *>(a.kv.v) + static_cast<long long>(r) * (HD * X::kBytes);
+        if constexpr (VW >= 4) {
+#pragma unroll
+          for (int i = 0; i < VW / 4; ++i) {
+            const uint4 x = r >= 0 ? ld_cache(reinterpret_cast<const uint4 *>(src) + i * 8 + g) : make_uint4(0, 0, 0, 0);
+            vw[s][4 * i] = x.x; vw[s][4 * i + 1] = x.y; vw[s][4 * i + 2] = x.z; vw[s][4 * i + 3] = x.w;
+          }
+        } else {
+          const uint2 x = r >= 0 ? ld_cache(reinterpret_cast<const uint2 *>(src) + g) : make_uint2(0, 0);
+          vw[s][0] = x.x; vw[s][1] = x.y;
+        }
+      }
+    };
+    int row = row_at(seg0 + warp), next = row_at(seg0 + warp + kAtWarps);
+    load_k(row);
+    load_v(row);
+
     // ---- Q: rotated, in pieces, in the layout of the product's B operand -----------------
     __syncthreads();  // the last item's shared memory is free
-    for (int r = warp; r < kRows; r += kAtWarps) {
+    {
+      constexpr int kPerRow = kAtThreads / kRows, kPairs = HD / 2 / kPerRow;
+      const int r = tid / kPerRow, part = tid % kPerRow;  // pairs part, part + kPerRow, .. of row r
       const int t = (r0 + r) / p.G, hq = h * p.G + (r0 + r) % p.G;
       const long long at_p = static_cast<long long>(pos) + t;
-      const bool row = r0 + r < p.R && t < n_rows;
-      const bool on = row && at_p >= 0 && (!a.rope || at_p < a.rope_len);
-      float x[HD / 32];
+      const bool on = r0 + r < p.R && t < n_rows && at_p >= 0 && (!a.rope || at_p < a.rope_len);
       const TIO *q = static_cast<const TIO *>(a.q) + b * a.qs.seq + t * a.qs.token + hq * a.qs.head;
+      float x[kPairs], y[kPairs];
 #pragma unroll
-      for (int i = 0; i < HD / 32; ++i) x[i] = on ? to_f(q[lane + 32 * i]) : 0.f;
+      for (int i = 0; i < kPairs; ++i) {
+        x[i] = on ? to_f(q[part + kPerRow * i]) : 0.f;
+        y[i] = on ? to_f(q[part + kPerRow * i + HD / 2]) : 0.f;
+      }
       if (a.rope && on) {
 #pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-          const float2 w = a.rope[at_p * (HD / 2) + lane + 32 * i];
-          const float lo = x[i], hi = x[i + HD / 64];
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 w = a.rope[at_p * (HD / 2) + part + kPerRow * i];
+          const float lo = x[i], hi = y[i];
           x[i] = lo * w.x - hi * w.y;
-          x[i + HD / 64] = hi * w.x + lo * w.y;
+          y[i] = hi * w.x + lo * w.y;
         }
       }
       float f = p.qscale;
       if constexpr (E4M3) {  // a power of two takes the row's largest value to [2^10, 2^11)
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < HD / 32; ++i) m = fmaxf(m, fabsf(x[i]));
+        for (int i = 0; i < kPairs; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = kPerRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int e = m < INFINITY ? max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) : 0;
 #pragma unroll
-        for (int i = 0; i < HD / 32; ++i) x[i] = ldexpf(x[i], 10 - e);
+        for (int i = 0; i < kPairs; ++i) {
+          x[i] = ldexpf(x[i], 10 - e);
+          y[i] = ldexpf(y[i], 10 - e);
+        }
         f = ldexpf(f, e - 10);
       }
 #pragma unroll
-      for (int i = 0; i < HD / 32; ++i) stage[r * HD + lane + 32 * i] = x[i];
-      if (lane == 0) {
+      for (int i = 0; i < kPairs; ++i) {
+        stage[r * HD + part + kPerRow * i] = x[i];
+        stage[r * HD + part + kPerRow * i + HD / 2] = y[i];
+      }
+      if (part == 0) {
         s_f[r] = f;
         s_lim[r] = on ? static_cast<int>(min(at_p, 0x7fffffffll)) : -1;
       }
     }
     __syncthreads();
+#pragma unroll 2
     for (int i = tid; i < KS * NT * 32; i += kAtThreads) {
       const int l = i % 32, n = i / 32 % NT, ks = i / 32 / NT;
-      const float *s = stage + (8 * n + l / 4) * HD + X::kdim(ks, l % 4);
+      const float4 s = *reinterpret_cast<const float4 *>(stage + (8 * n + l / 4) * HD + X::kdim(ks, l % 4));
       uint32_t w0[NQ], w1[NQ];
       if constexpr (E4M3) {
-        split_f16(s[0], s[1], w0);
-        split_f16(s[2], s[3], w1);
+        split_f16(s.x, s.y, w0);
+        split_f16(s.z, s.w, w1);
       } else {
-        split_bf16<NQ>(s[0], s[1], w0);
-        split_bf16<NQ>(s[2], s[3], w1);
+        split_bf16<NQ>(s.x, s.y, w0);
+        split_bf16<NQ>(s.z, s.w, w1);
       }
 #pragma unroll
       for (int k = 0; k < NQ; ++k) qfrag[((ks * NT + n) * NQ + k) * 32 + l] = make_uint2(w0[k], w1[k]);
@@ -587,64 +657,19 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[t][n][j] = 0.f;
     }
-    const int32_t *table = a.kv.page_table + static_cast<long long>(b) * a.kv.max_pages;
-    const long long all_see = static_cast<long long>(pos) + r0 / p.G;  // last position that every row sees
-    // pool row of position 16 unit + lane % 16, or -1
-    auto row_at = [&](int unit) {
-      const int q = unit * kUnit + (lane & 15);
-      if (unit >= seg1 || q >= len) return -1;
-      const int e = static_cast<int>((static_cast<unsigned long long>(q) * p.magic) >> p.shift);
-      const int page = table[e];
-      if (page < 0 || page >= a.kv.n_pages) return -1;
-      return (page * a.kv.n_kv_heads + h) * a.kv.page_size + (q - e * a.kv.page_size);
-    };
-    int row = row_at(seg0 + warp);
     for (int unit = seg0 + warp; unit < seg1; unit += kAtWarps) {
-      const int next = row_at(unit + kAtWarps);
+      const int after = row_at(unit + 2 * kAtWarps);
       const int p0 = unit * kUnit;
-      // loads of the whole unit
-      uint32_t kw[2][KW], vw[4][VW];
+      // S^T = K Q^T, one sum per piece of q while there are few tiles: the chains of
+      // dependent products are shorter
+      constexpr int kSums = NT <= 2 ? NQ : 1;
+      float sp[kSums][NT][4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int r = __shfl_sync(0xffffffffu, row, g + 8 * s);
-        const char *src = static_cast<const char *>(a.kv.k) + static_cast<long long>(r) * (HD * X::kBytes);
+      for (int i = 0; i < kSums; ++i)
 #pragma unroll
-        for (int i = 0; i < KW / 4; ++i) {
-          const uint4 x = r >= 0 ? ld_cache(reinterpret_cast<const uint4 *>(src) + i * 4 + c) : make_uint4(0, 0, 0, 0);
-          kw[s][4 * i] = x.x; kw[s][4 * i + 1] = x.y; kw[s][4 * i + 2] = x.z; kw[s][4 * i + 3] = x.w;
-        }
-      }
-      float ks_[2] = {1.f, 1.f}, vs_[2] = {1.f, 1.f};
-      if constexpr (E4M3) {
-        const float ks = row >= 0 ? a.kv.k_scale[row] : 0.f, vs = row >= 0 ? a.kv.v_scale[row] : 0.f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          ks_[s] = __shfl_sync(0xffffffffu, ks, g + 8 * s);
-          vs_[s] = __shfl_sync(0xffffffffu, vs, g + 8 * s);
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int r = __shfl_sync(0xffffffffu, row, 2 * c + (s & 1) + 8 * (s >> 1));
-        const char *src = static_cast<const char *>(a.kv.v) + static_cast<long long>(r) * (HD * X::kBytes);
-        if constexpr (VW >= 4) {
-#pragma unroll
-          for (int i = 0; i < VW / 4; ++i) {
-            const uint4 x = r >= 0 ? ld_cache(reinterpret_cast<const uint4 *>(src) + i * 8 + g) : make_uint4(0, 0, 0, 0);
-            vw[s][4 * i] = x.x; vw[s][4 * i + 1] = x.y; vw[s][4 * i + 2] = x.z; vw[s][4 * i + 3] = x.w;
-          }
-        } else {
-          const uint2 x = r >= 0 ? ld_cache(reinterpret_cast<const uint2 *>(src) + g) : make_uint2(0, 0);
-          vw[s][0] = x.x; vw[s][1] = x.y;
-        }
-      }
-
-      // S^T = K Q^T
-      float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+          for (int j = 0; j < 4; ++j) sp[i][n][j] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t a0, a1, a2, a3;
@@ -660,13 +685,31 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           a3 = kw[1][2 * k + 1];
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < NQ; ++i)
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) {
+          for (int n = 0; n < NT; ++n) {
             const uint2 q = qfrag[((k * NT + n) * NQ + i) * 32 + lane];
-            mma<E4M3>(s[n], a0, a1, a2, a3, q.x, q.y);
+            mma<E4M3>(sp[i % kSums][n], a0, a1, a2, a3, q.x, q.y);
           }
       }
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[n][j] = sp[kSums - 1][n][j];
+#pragma unroll
+          for (int i = kSums - 2; i >= 0; --i) s[n][j] += sp[i][n][j];
+        }
+      float ks_[2] = {1.f, 1.f}, vs_[2] = {1.f, 1.f};
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ks_[i] = __shfl_sync(0xffffffffu, ksc, g + 8 * i);
+          vs_[i] = __shfl_sync(0xffffffffu, vsc, g + 8 * i);
+        }
+      }
+      load_k(next);  // in flight through the softmax and the second product
 
       // scores (element j: position g + 8 (j / 2), row 2 c + j % 2 of tile n); masks
       const bool held = __all_sync(0xffffffffu, row >= 0);
@@ -800,11 +843,13 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           a3 = __byte_perm(vw[2][t], vw[3][t], 0x7632);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int k = 0; k < NP; ++k)
 #pragma unroll
-          for (int k = 0; k < NP; ++k) mma<false>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+          for (int n = 0; n < NT; ++n) mma<false>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
       }
+      load_v(next);  // in flight through the next first product
       row = next;
+      next = after;
     }
 
     // ---- the warps' sums under one reference, added in the warps' order --------------------
@@ -834,94 +879,104 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       s_L[tid] = L;
     }
     __syncthreads();
-    // element (e, g, row) at ((e * 8 + g) * kRows + row)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float by[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) by[j] = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - s_M[8 * n + 2 * c + j]);
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * n + 2 * c + j;
+        const float by = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - s_M[r]);
 #pragma unroll
-      for (int t = 0; t < KS; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float2 *>(merge + warp * (kRows * HD) + ((2 * t + e) * 8 + g) * kRows + 8 * n + 2 * c) =
-              make_float2(acc[t][n][2 * e] * by[0], acc[t][n][2 * e + 1] * by[1]);
+        for (int t = 0; t < KS; ++t)  // elements 2 t and 2 t + 1 are neighbouring dimensions
+          *reinterpret_cast<float2 *>(merge + (warp * kRows + r) * kLd + X::dim(g, 2 * t)) =
+              make_float2(acc[t][n][j] * by, acc[t][n][2 + j] * by);
+      }
     }
     __syncthreads();
 
-    // writes element i of the item's output, given its sum and its row's sum of weights
-    auto finish = [&](int i, float x, float L) {
-      const int r = i % kRows, e = i / kRows / 8, gg = i / kRows % 8;
+    // From here on a thread holds pairs of dimensions: pair i of the item's kRows x HD.
+    constexpr int kPairsAll = kRows * HD / 2, kPer = kPairsAll / kAtThreads;
+    auto finish = [&](int i, float2 x, float L) {
+      const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
       const int t = (r0 + r) / p.G, hq = h * p.G + (r0 + r) % p.G;
       if (r0 + r >= p.R || t >= n_rows) return;
-      const float y = s_lim[r] < 0 || L == 0.f ? 0.f : x / L;
-      const long long o = ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * HD + X::dim(gg, e);
-      if constexpr (sizeof(TIO) == 4) static_cast<float *>(a.out)[o] = y;
-      else static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(y);
+      const bool none = s_lim[r] < 0 || L == 0.f;
+      const float2 y = none ? make_float2(0.f, 0.f) : make_float2(x.x / L, x.y / L);
+      const long long o = ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * HD + d;
+      if constexpr (sizeof(TIO) == 4) {  // a caller's out may start on any element
+        static_cast<float *>(a.out)[o] = y.x;
+        static_cast<float *>(a.out)[o + 1] = y.y;
+      } else {
+        static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(y.x);
+        static_cast<__nv_bfloat16 *>(a.out)[o + 1] = __float2bfloat16_rn(y.y);
+      }
     };
     auto summed = [&](int i) {
-      float x = merge[i];
+      const float *src = merge + i / (HD / 2) * kLd + 2 * (i % (HD / 2));
+      float2 x = *reinterpret_cast<const float2 *>(src);
 #pragma unroll
-      for (int w = 1; w < kAtWarps; ++w) x += merge[w * (kRows * HD) + i];
+      for (int w = 1; w < kAtWarps; ++w) {
+        const float2 y = *reinterpret_cast<const float2 *>(src + w * kRows * kLd);
+        x.x += y.x;
+        x.y += y.y;
+      }
       return x;
     };
     if (whole) {
-      for (int i = tid; i < kRows * HD; i += kAtThreads) finish(i, summed(i), s_L[i % kRows]);
+#pragma unroll
+      for (int i = tid; i < kPairsAll; i += kAtThreads) finish(i, summed(i), s_L[i / (HD / 2)]);
     } else {
       // ---- this block's part of the item, and the join by the last to leave one ------------
       const int first = block_of(at), last = block_of(at + cost - 1), me = blockIdx.x;
       // slot 1: the item begins in this block; slot 0: it began before
-      const int slot = 2 * me + (seg0 == 0);
-      float *dst = p.part + static_cast<long long>(slot) * (kRows * HD);
-      float *ml = p.part_ml + static_cast<long long>(slot) * (2 * kRows);
-      for (int i = tid; i < kRows * HD; i += kAtThreads) __stcg(dst + i, summed(i));
-      if (tid < kRows) {
-        __stcg(ml + 2 * tid, s_M[tid]);
-        __stcg(ml + 2 * tid + 1, s_L[tid]);
-      }
       auto slot_of = [&](int blk) { return 2 * blk + (blk == first); };
-      // joins the parts of blocks b0, b0 + step, .. <= b1; `out`: the item's output, else
-      // back into b0's part
+      float2 *dst = reinterpret_cast<float2 *>(p.part) + static_cast<long long>(slot_of(me)) * kPairsAll;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) __stcg(dst + tid + i * kAtThreads, summed(tid + i * kAtThreads));
+      if (tid < kRows) __stcg(p.part_ml + slot_of(me) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
+      // joins the parts of blocks b0, b0 + step, .. <= b1 (at most kJoin, or any number
+      // on the second level); `out`: into the item's output, else back into b0's part
       auto join = [&](int b0, int b1, int step, bool out) {
         __syncthreads();
-        if (tid < kRows) {
+        const int parts = (b1 - b0) / step + 1;
+        for (int i = tid; i < kRows; i += kAtThreads) {
           float M = -INFINITY, L = 0.f;
-          for (int k = b0; k <= b1; k += step) M = fmaxf(M, __ldcg(p.part_ml + slot_of(k) * (2 * kRows) + 2 * tid));
-          for (int k = b0; k <= b1; k += step) {
-            const float mk = __ldcg(p.part_ml + slot_of(k) * (2 * kRows) + 2 * tid);
-            const float lk = __ldcg(p.part_ml + slot_of(k) * (2 * kRows) + 2 * tid + 1);
-            L += mk == -INFINITY ? lk : lk * ex2(mk - M);
+#pragma unroll 8
+          for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(p.part_ml + slot_of(b0 + k * step) * kRows + i).x);
+#pragma unroll 8
+          for (int k = 0; k < parts; ++k) {
+            const float2 ml = __ldcg(p.part_ml + slot_of(b0 + k * step) * kRows + i);
+            L += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - M);
           }
-          s_M[tid] = M;
-          s_L[tid] = L;
+          s_M[i] = M;
+          s_L[i] = L;
         }
         __syncthreads();
-        constexpr int kPer = kRows * HD / kAtThreads;
-        const int r = tid % kRows;  // kAtThreads is a multiple of kRows
-        float x[kPer];
+        float2 x[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = 0.f;
-        const float M = s_M[r];
-#pragma unroll 2
-        for (int k = b0; k <= b1; k += step) {
-          const float mk = __ldcg(p.part_ml + slot_of(k) * (2 * kRows) + 2 * r);
-          const float by = mk == -INFINITY ? 1.f : ex2(mk - M);
-          const float *src = p.part + static_cast<long long>(slot_of(k)) * (kRows * HD);
+        for (int i = 0; i < kPer; ++i) x[i] = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+          const int sl = slot_of(b0 + k * step);
+          const float2 *src = reinterpret_cast<const float2 *>(p.part) + static_cast<long long>(sl) * kPairsAll;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) x[i] = fmaf(__ldcg(src + tid + i * kAtThreads), by, x[i]);
+          for (int i = 0; i < kPer; ++i) {
+            const int r = (tid + i * kAtThreads) / (HD / 2);
+            const float mk = __ldcg(p.part_ml + sl * kRows + r).x;
+            const float by = mk == -INFINITY ? 1.f : ex2(mk - s_M[r]);
+            const float2 y = __ldcg(src + tid + i * kAtThreads);
+            x[i].x = fmaf(y.x, by, x[i].x);
+            x[i].y = fmaf(y.y, by, x[i].y);
+          }
         }
-        __syncthreads();
         if (out) {
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) finish(tid + i * kAtThreads, x[i], s_L[r]);
+          for (int i = 0; i < kPer; ++i) finish(tid + i * kAtThreads, x[i], s_L[(tid + i * kAtThreads) / (HD / 2)]);
         } else {
-          float *o = p.part + static_cast<long long>(slot_of(b0)) * (kRows * HD);
+          float2 *o = reinterpret_cast<float2 *>(p.part) + static_cast<long long>(slot_of(b0)) * kPairsAll;
+          __syncthreads();  // every thread has read b0's reference
 #pragma unroll
           for (int i = 0; i < kPer; ++i) __stcg(o + tid + i * kAtThreads, x[i]);
-          if (tid < kRows) {
-            __stcg(p.part_ml + slot_of(b0) * (2 * kRows) + 2 * tid, s_M[tid]);
-            __stcg(p.part_ml + slot_of(b0) * (2 * kRows) + 2 * tid + 1, s_L[tid]);
-          }
+          if (tid < kRows) __stcg(p.part_ml + slot_of(b0) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
         }
       };
       // arrives at a counter of `n`; true in every thread of the block that is last
@@ -1022,7 +1077,7 @@ static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStr
   p.n_rg = (p.R + S::kRows - 1) / S::kRows;
   p.count = static_cast<uint32_t *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + count_bytes(n_sm));
-  p.part_ml = p.part + static_cast<size_t>(2) * blocks * S::kRows * HD;
+  p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD);
   if (S::kSmem > 46 * 1024) {
     static std::atomic<uint64_t> done{0};  // devices on which the size is set
     int dev = 0;
