@@ -1006,6 +1006,7 @@ MK_API int mk_paged_attention(const mk_paged_kv *kv, const void *q, mk_strides q
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads)
     return fail(MK_ERR_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
   if ((long long)T * n_q_heads >= (1ll << 30)) return fail(MK_ERR_UNSUPPORTED, "T * n_q_heads must be below 2^30");
+  if (!aligned(out, 16)) return fail(MK_ERR_ARG, "out must be 16-byte aligned");
   if (!std::isfinite(scale)) return fail(MK_ERR_ARG, "scale must be finite");
   if (!workspace || !aligned(workspace, 16)) return fail(MK_ERR_ARG, "workspace must be given, 16-byte aligned");
   int n_sm = 0;

@@ -279,13 +279,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_gather(const __grid_constant__
 // out two pieces (2^-16 of it) are well under the output's rounding of 2^-8.
 // Everything else is fp32.
 // ---------------------------------------------------------------------------
-constexpr int kAtWarps = 4;
-constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kUnit = 16;          // positions per unit
 constexpr float kLazy = 8.0f;      // a score may pass its row's reference by 2^8 before it is moved
-constexpr int kAtMaxBlocks = 3;    // resident blocks per SM, at most
-constexpr int kMinUnits = 8;       // units per block, at least: two a warp
-constexpr int kJoin = 16;          // blocks of an item joined by one; more are joined in two levels
+constexpr int kMinUnits = 8;       // units per block, at least
+constexpr int kLongShare = 64;     // units per block from which items are cut anywhere
+constexpr int kJoin = 32;          // blocks of an item joined by one; more are joined in two levels
+constexpr int kAtMaxBlocks = kJoin * kJoin;  // blocks of a grid, at most
 
 template <int HD, bool E4M3>
 struct Geo {
@@ -306,25 +305,35 @@ struct Geo {
 template <int HD, typename TIO, bool E4M3, int NT>
 struct AtShape {
   static constexpr int kRows = 8 * NT;
+  static constexpr int kWarps = 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kBlocks = NT == 1 ? 3 : 2;   // resident per SM: what registers allow
   static constexpr int NQ = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int NP = sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int kQBytes = Geo<HD, E4M3>::KS * NQ * NT * 32 * 8;      // fragments of Q^T
   static constexpr int kStage = kRows * HD * 4;                             // rotated q, fp32
-  static constexpr int kLd = HD + 2;                                        // row stride of the warps' sums
-  static constexpr int kMerge = kAtWarps * kRows * kLd * 4;
+  static constexpr int kLd = HD + 4;                                        // row stride of the warps' sums
+  static constexpr int kMerge = kWarps * kRows * kLd * 4;
   static constexpr int kSmem = kMerge > kQBytes + kStage ? kMerge : kQBytes + kStage;
-  static constexpr int kBlocks = NT == 1 ? 3 : 2;                           // resident per SM
+};
+
+struct Div {  // x / d = (x magic) >> shift for 0 <= x < 2^31
+  uint32_t magic, shift;
+  __device__ __forceinline__ int of(int x) const {
+    return static_cast<int>((static_cast<unsigned long long>(x) * magic) >> shift);
+  }
 };
 
 struct AttnArgs {
   PagedAttn a;
   int G, R, n_rg;            // query heads of a KV head, rows of a KV head, row groups
-  uint32_t magic, shift;     // p / page_size = (p * magic) >> shift for 0 <= p < 2^31
+  int few;                   // up to 32 sequences of one row group each, units below 2^31
+  Div by_page, by_G;
   int cap;                   // positions of a page table's row
   float qscale;              // scale * log2(e)
-  float *part;               // [2 * blocks][kRows][HD] sums
+  float4 *part;              // [2 * blocks][kRows][HD / 4] sums
   float2 *part_ml;           // [2 * blocks][kRows] (reference, sum of weights)
-  uint32_t *count;           // [blocks] per item, then [2 * blocks] per group of the first level
+  uint32_t *count;           // [kAtMaxBlocks] per item, then [2 * kAtMaxBlocks] per group of a join's first level
 };
 
 __device__ __forceinline__ uint4 ld_cache(const uint4 *p) {
@@ -403,47 +412,167 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t (&w)[2]) {
   w[1] = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-struct Item {
-  int b, rg, h;      // sequence, row group, KV head
-  int len, cost;     // positions to visit, units
-};
-
 __device__ __forceinline__ int seq_rows(const PagedAttn &a, int b) {
   return a.counts ? max(0, min(a.counts[b], a.T)) : a.T;
 }
 
 // Positions that row group rg of sequence b visits (-1: it has no rows).
 __device__ __forceinline__ int group_len(const AttnArgs &p, int rows, int b, int rg) {
-  const int n = seq_rows(p.a, b), t0 = rg * rows / p.G;
+  const int n = seq_rows(p.a, b);
+  int t0 = 0, t1 = n - 1;
+  if (p.n_rg > 1) {
+    t0 = p.by_G.of(rg * rows);
+    t1 = min(p.by_G.of(min(p.R, (rg + 1) * rows) - 1), t1);
+  }
   if (t0 >= n) return -1;
-  const int t1 = min((min(p.R, (rg + 1) * rows) - 1) / p.G, n - 1);
   const long long len = static_cast<long long>(p.a.positions[b]) + t1 + 1;
   return static_cast<int>(max(0ll, min(len, static_cast<long long>(p.cap))));
 }
 
 __device__ __forceinline__ int units_of(int len) { return len < 0 ? 0 : max(1, (len + kUnit - 1) / kUnit); }
 
-__device__ __forceinline__ long long seq_units(const AttnArgs &p, int rows, int b) {
-  long long n = 0;
-  for (int rg = 0; rg < p.n_rg; ++rg) n += units_of(group_len(p, rows, b, rg));
-  return n * p.a.kv.n_kv_heads;
+// Weight of an item of n units when parts hold up to `size`.
+__device__ __forceinline__ int weight_of(int n, int size) { return size == 1 ? n : (n + size - 1) / size; }
+
+// The size of the parts.  Long shares (kLongShare units a block): 1, the line of
+// units is cut into equal shares, an item wherever one ends.  Short ones: a second
+// item in a block costs more than uneven parts do (8 us of a block's 25 for 32
+// sequences of 512 to 2048), so each item is cut into equal parts, one a block, of a
+// size for which the blocks suffice: parts <= units / size + items <= blocks.
+__device__ __forceinline__ int part_size(int units, int items, int grid) {
+  return units >= grid * kLongShare || items >= grid ? 1 : max(kMinUnits, (units + grid - items - 1) / (grid - items));
+}
+
+// A block's place: weights [u0, u1) of the line, of which sequence b's first is `at`.
+// Shares hold `share` weights, the first `more` of them one more.
+struct Place {
+  long long u0, u1, at, share, more;
+  int size, b;  // b < 0: nothing
+};
+
+__device__ __forceinline__ void share_out(Place &w, long long line, int grid) {
+  const long long nb = min(static_cast<long long>(grid), w.size > 1 ? line : (line + kMinUnits - 1) / kMinUnits);
+  w.share = line / max(nb, 1ll);
+  w.more = line - w.share * nb;
+  w.u0 = blockIdx.x * w.share + min(static_cast<long long>(blockIdx.x), w.more);
+  w.u1 = blockIdx.x < nb ? w.u0 + w.share + (blockIdx.x < w.more) : w.u0;
+}
+
+// Any number of sequences and row groups; s_scan: kWarps + 2 words of shared memory.
+template <int THREADS>
+__device__ __noinline__ Place place_of_many(const AttnArgs &p, int rows, long long *s_scan) {
+  constexpr int kWarps = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.a.B;
+  auto seq_weight = [&](int b, int size) {
+    long long n = 0;
+#pragma unroll 1
+    for (int rg = 0; rg < p.n_rg; ++rg) n += weight_of(units_of(group_len(p, rows, b, rg)), size);
+    return n * p.a.kv.n_kv_heads;
+  };
+  Place w{};
+  w.size = 1;
+  w.b = -1;
+  long long line = 0;
+  // pass 0: the units; 1: the weights, where parts are not single units; 2: the place
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    if (pass == 1) {
+      const long long items = static_cast<long long>(B) * p.n_rg * p.a.kv.n_kv_heads, grid = gridDim.x;
+      if (items < grid && line < grid * kLongShare) w.size = part_size(static_cast<int>(line), static_cast<int>(items), gridDim.x);
+      if (w.size == 1) continue;
+    }
+    if (pass == 2) {
+      share_out(w, line, gridDim.x);
+      if (w.u0 == w.u1) return w;
+    }
+    long long base = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += THREADS) {
+      const long long n = b0 + tid < B ? seq_weight(b0 + tid, w.size) : 0;
+      long long incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = incl;
+      if (tid == 0) s_scan[kWarps] = -1;
+      __syncthreads();
+      incl += base;
+      for (int k = 0; k < kWarps; ++k) {
+        if (k < warp) incl += s_scan[k];
+        base += s_scan[k];
+      }
+      if (pass == 2) {
+        if (n > 0 && incl - n <= w.u0 && w.u0 < incl) {
+          s_scan[kWarps] = b0 + tid;
+          s_scan[kWarps + 1] = incl - n;
+        }
+        __syncthreads();
+        if (s_scan[kWarps] >= 0) {
+          w.b = static_cast<int>(s_scan[kWarps]);
+          w.at = s_scan[kWarps + 1];
+          break;
+        }
+      }
+    }
+    if (pass < 2) line = base;
+  }
+  return w;
+}
+
+// Up to 32 sequences of one row group each: every warp counts for itself.
+__device__ __forceinline__ Place place_of_few(const AttnArgs &p, int rows) {
+  const int lane = threadIdx.x & 31, hkv = p.a.kv.n_kv_heads, grid = gridDim.x;
+  const int units = lane < p.a.B ? units_of(group_len(p, rows, lane, 0)) : 0;
+  int line = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units * hkv)));
+  Place w{};
+  w.size = part_size(line, p.a.B * hkv, grid);
+  const int n = weight_of(units, w.size) * hkv;
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  line = __shfl_sync(0xffffffffu, incl, 31);
+  const int nb = max(1, min(grid, w.size > 1 ? line : (line + kMinUnits - 1) / kMinUnits)), me = blockIdx.x;
+  const int share = w.size > 1 ? 1 : line / nb, more = line - share * nb;
+  const int u0 = me * share + min(me, more), u1 = me < nb ? u0 + share + (me < more) : u0;
+  const unsigned hit = __ballot_sync(0xffffffffu, u0 < u1 && incl - n <= u0 && u0 < incl);
+  w.share = share;
+  w.more = more;
+  w.u0 = u0;
+  w.u1 = u1;
+  w.b = hit ? __ffs(hit) - 1 : -1;
+  w.at = __shfl_sync(0xffffffffu, incl - n, hit ? w.b : 0);
+  return w;
+}
+
+// The block whose share holds weight u.
+__device__ __noinline__ int block_of(long long u, long long share, long long more) {
+  const long long cut = more * (share + 1);
+  const bool low = u < cut;
+  return static_cast<int>((low ? 0 : more) + (low ? u : u - cut) / (low ? share + 1 : share));
 }
 
 template <int HD, typename TIO, bool E4M3, int NT>
-__global__ void __launch_bounds__(kAtThreads, (AtShape<HD, TIO, E4M3, NT>::kBlocks))
+__global__ void __launch_bounds__((AtShape<HD, TIO, E4M3, NT>::kThreads), (AtShape<HD, TIO, E4M3, NT>::kBlocks))
 paged_attn(const __grid_constant__ AttnArgs p) {
   using S = AtShape<HD, TIO, E4M3, NT>;
   using X = Geo<HD, E4M3>;
-  constexpr int kRows = S::kRows, NQ = S::NQ, NP = S::NP, KS = X::KS, KW = X::KW, VW = X::VW, kLd = S::kLd;
+  constexpr int kRows = S::kRows, NQ = S::NQ, NP = S::NP, KS = X::KS, KW = X::KW, VW = X::VW, kLd = S::kLd,
+                kAtWarps = S::kWarps, kAtThreads = S::kThreads;
   extern __shared__ __align__(16) unsigned char dyn[];
-  __shared__ long long s_scan[kAtWarps];
-  __shared__ long long s_at;
-  __shared__ int s_b;
+  __shared__ long long s_scan[kAtWarps + 2];
   __shared__ float s_f[kRows];                  // factor of a row's scores
   __shared__ int s_lim[kRows];                  // last position a row sees, -1: none
   __shared__ float s_m[kAtWarps][kRows], s_l[kAtWarps][kRows];
   __shared__ float s_M[kRows], s_L[kRows];
+  __shared__ long long s_out[kRows];            // first element of a row of the output, -1: no such row
   __shared__ uint32_t s_last;
+  __shared__ int s_bad;
   uint2 *qfrag = reinterpret_cast<uint2 *>(dyn);
   float *stage = reinterpret_cast<float *>(dyn + S::kQBytes);
   float *merge = reinterpret_cast<float *>(dyn);
@@ -452,65 +581,19 @@ paged_attn(const __grid_constant__ AttnArgs p) {
   pdl_wait();
   pdl_launch();
 
-  // ---- this block's share of the units, and the sequence that holds its first ------------
-  // inclusive sum of n over the block's threads, and over all of them
-  auto block_scan = [&](long long n, long long &all) {
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kAtWarps; ++w) {
-      if (w < warp) incl += s_scan[w];
-      all += s_scan[w];
-    }
-    return incl;
-  };
-  long long total = 0, n = 0, incl = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
-    long long all;
-    n = b0 + tid < a.B ? seq_units(p, kRows, b0 + tid) : 0;
-    incl = block_scan(n, all);
-    total += all;
-  }
-  if (total == 0) return;
-  const long long nb = min(static_cast<long long>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
-  if (blockIdx.x >= nb) return;
-  const long long u0 = blockIdx.x * total / nb, u1 = (blockIdx.x + 1) * total / nb;
-  auto block_of = [&](long long u) { return static_cast<int>(((u + 1) * nb - 1) / total); };
-  if (tid == 0) s_b = -1;
-  __syncthreads();
-  long long base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
-    if (a.B > kAtThreads) {  // else n and incl are still those of the only pass
-      long long all;
-      n = b0 + tid < a.B ? seq_units(p, kRows, b0 + tid) : 0;
-      incl = block_scan(n, all) + base;
-      base += all;
-    }
-    if (n > 0 && incl - n <= u0 && u0 < incl) {
-      s_b = b0 + tid;
-      s_at = incl - n;
-    }
-    __syncthreads();
-    if (s_b >= 0) break;
-  }
-  int b = s_b, rg = 0, h = 0;
-  long long at = s_at;  // first unit of item (b, rg, h)
+  const Place place = p.few ? place_of_few(p, kRows) : place_of_many<kAtThreads>(p, kRows, s_scan);
+  if (place.b < 0) return;
+  int b = place.b, rg = 0, h = 0;
+  long long at = place.at;  // first weight of item (b, rg, h)
 
-  for (long long u = u0; u < u1;) {
-    // the item that holds unit u: row groups in order, each with all KV heads
+  for (long long u = place.u0; u < place.u1;) {
+    // the item that holds weight u: row groups in order, each with all KV heads
     int len = group_len(p, kRows, b, rg);
-    int cost = units_of(len);
-    while (at + cost <= u) {
-      at += cost;
-      if (cost == 0 || ++h == a.kv.n_kv_heads) {
+    int cost = units_of(len), weight = weight_of(cost, place.size);
+#pragma unroll 1
+    while (at + weight <= u) {
+      at += weight;
+      if (weight == 0 || ++h == a.kv.n_kv_heads) {
         h = 0;
         if (++rg == p.n_rg) {
           rg = 0;
@@ -518,23 +601,28 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         }
         len = group_len(p, kRows, b, rg);
         cost = units_of(len);
+        weight = weight_of(cost, place.size);
       }
     }
-    const int seg0 = static_cast<int>(u - at), seg1 = static_cast<int>(min(u1 - at, static_cast<long long>(cost)));
+    const int w0 = static_cast<int>(u - at), w1 = static_cast<int>(min(place.u1 - at, static_cast<long long>(weight)));
+    // units [seg0, seg1) of the item; parts of equal size (products below 2^31: short lines only)
+    const int seg0 = place.size == 1 ? w0 : w0 * cost / weight, seg1 = place.size == 1 ? w1 : w1 * cost / weight;
     const bool whole = seg0 == 0 && seg1 == cost;
     const int pos = a.positions[b], n_rows = seq_rows(a, b), r0 = rg * kRows;
 
     // ---- loads of a unit, a whole one ahead of its products ------------------------------
     const int32_t *table = a.kv.page_table + static_cast<long long>(b) * a.kv.max_pages;
-    const long long all_see = static_cast<long long>(pos) + r0 / p.G;  // last position that every row sees
-    // pool row of position 16 unit + lane % 16, or -1
-    auto row_at = [&](int unit) {
-      const int q = unit * kUnit + (lane & 15);
-      if (unit >= seg1 || q >= len) return -1;
-      const int e = static_cast<int>((static_cast<unsigned long long>(q) * p.magic) >> p.shift);
+    const long long all_see = static_cast<long long>(pos) + p.by_G.of(r0);  // last position that every row sees
+    // pool row of position q, and of position 16 unit + lane % 16; -1: none
+    auto row_of = [&](int q) {
+      const int e = p.by_page.of(q);
       const int page = table[e];
       if (page < 0 || page >= a.kv.n_pages) return -1;
       return (page * a.kv.n_kv_heads + h) * a.kv.page_size + (q - e * a.kv.page_size);
+    };
+    auto row_at = [&](int unit) {
+      const int q = unit * kUnit + (lane & 15);
+      return unit >= seg1 || q >= len ? -1 : row_of(q);
     };
     uint32_t kw[2][KW], vw[4][VW];
     float ksc = 0.f, vsc = 0.f;  // scales of position lane % 16
@@ -572,31 +660,39 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       }
     };
     int row = row_at(seg0 + warp), next = row_at(seg0 + warp + kAtWarps);
-    load_k(row);
-    load_v(row);
 
     // ---- Q: rotated, in pieces, in the layout of the product's B operand -----------------
-    __syncthreads();  // the last item's shared memory is free
     {
       constexpr int kPerRow = kAtThreads / kRows, kPairs = HD / 2 / kPerRow;
       const int r = tid / kPerRow, part = tid % kPerRow;  // pairs part, part + kPerRow, .. of row r
-      const int t = (r0 + r) / p.G, hq = h * p.G + (r0 + r) % p.G;
+      const int t = p.by_G.of(r0 + r), hq = h * p.G + (r0 + r) - t * p.G;
       const long long at_p = static_cast<long long>(pos) + t;
-      const bool on = r0 + r < p.R && t < n_rows && at_p >= 0 && (!a.rope || at_p < a.rope_len);
-      const TIO *q = static_cast<const TIO *>(a.q) + b * a.qs.seq + t * a.qs.token + hq * a.qs.head;
+      const bool is_row = r0 + r < p.R && t < n_rows;
+      const bool on = is_row && at_p >= 0 && (!a.rope || at_p < a.rope_len);
+      const TIO *q = static_cast<const TIO *>(a.q) + b * a.qs.seq + t * a.qs.token + hq * a.qs.head + part;
+      const float2 *cs = a.rope + at_p * (HD / 2) + part;
+      const bool turn = a.rope && on;
+      TIO lo[kPairs], hi[kPairs];
+      float2 w[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        lo[i] = on ? q[kPerRow * i] : TIO(0.f);
+        hi[i] = on ? q[kPerRow * i + HD / 2] : TIO(0.f);
+        w[i] = turn ? cs[kPerRow * i] : make_float2(1.f, 0.f);
+      }
+      load_k(row);  // the first unit's loads wait for its page's number; the rows' are on their way
+      load_v(row);
       float x[kPairs], y[kPairs];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        x[i] = on ? to_f(q[part + kPerRow * i]) : 0.f;
-        y[i] = on ? to_f(q[part + kPerRow * i + HD / 2]) : 0.f;
+        x[i] = to_f(lo[i]) * w[i].x - to_f(hi[i]) * w[i].y;
+        y[i] = to_f(hi[i]) * w[i].x + to_f(lo[i]) * w[i].y;
       }
-      if (a.rope && on) {
+      if (!a.rope) {  // exactly the row, infinities too
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const float2 w = a.rope[at_p * (HD / 2) + part + kPerRow * i];
-          const float lo = x[i], hi = y[i];
-          x[i] = lo * w.x - hi * w.y;
-          y[i] = hi * w.x + lo * w.y;
+          x[i] = to_f(lo[i]);
+          y[i] = to_f(hi[i]);
         }
       }
       float f = p.qscale;
@@ -607,13 +703,15 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
         for (int o = kPerRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int e = m < INFINITY ? max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) : 0;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          x[i] = ldexpf(x[i], 10 - e);
-          y[i] = ldexpf(y[i], 10 - e);
+          x[i] *= up;
+          y[i] *= up;
         }
-        f = ldexpf(f, e - 10);
+        f *= __uint_as_float(static_cast<uint32_t>(127 + e - 10) << 23);
       }
+      __syncthreads();  // the last item's shared memory is free
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         stage[r * HD + part + kPerRow * i] = x[i];
@@ -622,10 +720,12 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       if (part == 0) {
         s_f[r] = f;
         s_lim[r] = on ? static_cast<int>(min(at_p, 0x7fffffffll)) : -1;
+        s_out[r] = is_row ? ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * HD : -1;
       }
+      if (tid == 0) s_bad = 0;
     }
     __syncthreads();
-#pragma unroll 2
+#pragma unroll 1
     for (int i = tid; i < KS * NT * 32; i += kAtThreads) {
       const int l = i % 32, n = i / 32 % NT, ks = i / 32 / NT;
       const float4 s = *reinterpret_cast<const float4 *>(stage + (8 * n + l / 4) * HD + X::kdim(ks, l % 4));
@@ -763,56 +863,27 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           s[n][j] = !E4M3 || x == -INFINITY ? w : w * vs_[j >> 1];
         }
       if (!full) {
-        // V values that only some rows see are multiplied by the others' zero weights:
-        // where one is not finite, those positions are added value by value instead.
+        // V values that only some rows see meet the others' zero weights: one that is not
+        // finite is taken out here, and put into the rows that see it below.
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
+          if (p0 + 2 * c + (i & 1) + 8 * (i >> 1) > all_see)
 #pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            const uint32_t x = vw[i][w];
-            if (E4M3)
-              bad = bad || (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);
-            else
-              bad = bad || (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
-          }
-        if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (p0 + 2 * c + (i & 1) + 8 * (i >> 1) > all_see)
-#pragma unroll
-              for (int w = 0; w < VW; ++w) vw[i][w] = 0;
-          for (int i = 0; i < kUnit; ++i) {
-            const int r = __shfl_sync(0xffffffffu, row, i);
-            if (r < 0 || p0 + i <= all_see) continue;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float w[2];
-              bool sees[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                w[j] = __shfl_sync(0xffffffffu, i < 8 ? s[n][j] : s[n][j + 2], (i & 7) * 4 + c);
-                sees[j] = p0 + i <= s_lim[8 * n + 2 * c + j];
+            for (int w = 0; w < VW; ++w) {
+              const uint32_t x = vw[i][w];
+              uint32_t keep = 0xffffffffu;
+              if constexpr (E4M3) {
+                const uint32_t nan = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                keep = ~((nan >> 7) * 255u);
+              } else {
+                if ((x & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                if ((x & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
               }
-#pragma unroll
-              for (int t = 0; t < KS; ++t)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const long long o = static_cast<long long>(r) * HD + X::dim(g, 2 * t + e);
-                  float v;
-                  if constexpr (E4M3) {
-                    const uint32_t hv = codes_f16(static_cast<const uint8_t *>(a.kv.v)[o]);
-                    v = __half2float(__ushort_as_half(static_cast<unsigned short>(hv)));
-                  } else {
-                    v = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.kv.v)[o]);
-                  }
-#pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    if (sees[j]) acc[t][n][2 * e + j] = fmaf(w[j], v, acc[t][n][2 * e + j]);
-                }
+              vw[i][w] = x & keep;
+              bad = bad || keep != 0xffffffffu;
             }
-          }
-        }
+        if (bad) s_bad = 1;
       }
 
       // O^T += V^T P^T
@@ -886,124 +957,154 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         const int r = 8 * n + 2 * c + j;
         const float by = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - s_M[r]);
 #pragma unroll
-        for (int t = 0; t < KS; ++t)  // elements 2 t and 2 t + 1 are neighbouring dimensions
-          *reinterpret_cast<float2 *>(merge + (warp * kRows + r) * kLd + X::dim(g, 2 * t)) =
-              make_float2(acc[t][n][j] * by, acc[t][n][2 + j] * by);
+        for (int t = 0; t < KS; t += 2)  // elements 2 t .. 2 t + 3 are neighbouring dimensions
+          *reinterpret_cast<float4 *>(merge + (warp * kRows + r) * kLd + X::dim(g, 2 * t)) =
+              make_float4(acc[t][n][j] * by, acc[t][n][2 + j] * by, acc[t + 1][n][j] * by, acc[t + 1][n][2 + j] * by);
       }
     }
     __syncthreads();
 
-    // From here on a thread holds pairs of dimensions: pair i of the item's kRows x HD.
-    constexpr int kPairsAll = kRows * HD / 2, kPer = kPairsAll / kAtThreads;
-    auto finish = [&](int i, float2 x, float L) {
-      const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
-      const int t = (r0 + r) / p.G, hq = h * p.G + (r0 + r) % p.G;
-      if (r0 + r >= p.R || t >= n_rows) return;
-      const bool none = s_lim[r] < 0 || L == 0.f;
-      const float2 y = none ? make_float2(0.f, 0.f) : make_float2(x.x / L, x.y / L);
-      const long long o = ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * HD + d;
-      if constexpr (sizeof(TIO) == 4) {  // a caller's out may start on any element
-        static_cast<float *>(a.out)[o] = y.x;
-        static_cast<float *>(a.out)[o + 1] = y.y;
-      } else {
-        static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(y.x);
-        static_cast<__nv_bfloat16 *>(a.out)[o + 1] = __float2bfloat16_rn(y.y);
-      }
-    };
+    // From here on a thread holds four neighbouring dimensions: piece i of the item's kRows x HD.
+    constexpr int kPieces = kRows * HD / 4, kRowPieces = HD / 4;
     auto summed = [&](int i) {
-      const float *src = merge + i / (HD / 2) * kLd + 2 * (i % (HD / 2));
-      float2 x = *reinterpret_cast<const float2 *>(src);
+      const float *src = merge + i / kRowPieces * kLd + 4 * (i % kRowPieces);
+      float4 x = *reinterpret_cast<const float4 *>(src);
 #pragma unroll
       for (int w = 1; w < kAtWarps; ++w) {
-        const float2 y = *reinterpret_cast<const float2 *>(src + w * kRows * kLd);
+        const float4 y = *reinterpret_cast<const float4 *>(src + w * kRows * kLd);
         x.x += y.x;
         x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
       }
       return x;
     };
-    if (whole) {
-#pragma unroll
-      for (int i = tid; i < kPairsAll; i += kAtThreads) finish(i, summed(i), s_L[i / (HD / 2)]);
-    } else {
-      // ---- this block's part of the item, and the join by the last to leave one ------------
-      const int first = block_of(at), last = block_of(at + cost - 1), me = blockIdx.x;
-      // slot 1: the item begins in this block; slot 0: it began before
-      auto slot_of = [&](int blk) { return 2 * blk + (blk == first); };
-      float2 *dst = reinterpret_cast<float2 *>(p.part) + static_cast<long long>(slot_of(me)) * kPairsAll;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) __stcg(dst + tid + i * kAtThreads, summed(tid + i * kAtThreads));
-      if (tid < kRows) __stcg(p.part_ml + slot_of(me) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
-      // joins the parts of blocks b0, b0 + step, .. <= b1 (at most kJoin, or any number
-      // on the second level); `out`: into the item's output, else back into b0's part
-      auto join = [&](int b0, int b1, int step, bool out) {
-        __syncthreads();
-        const int parts = (b1 - b0) / step + 1;
-        for (int i = tid; i < kRows; i += kAtThreads) {
-          float M = -INFINITY, L = 0.f;
-#pragma unroll 8
-          for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(p.part_ml + slot_of(b0 + k * step) * kRows + i).x);
-#pragma unroll 8
-          for (int k = 0; k < parts; ++k) {
-            const float2 ml = __ldcg(p.part_ml + slot_of(b0 + k * step) * kRows + i);
-            L += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - M);
-          }
-          s_M[i] = M;
-          s_L[i] = L;
-        }
-        __syncthreads();
-        float2 x[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-          const int sl = slot_of(b0 + k * step);
-          const float2 *src = reinterpret_cast<const float2 *>(p.part) + static_cast<long long>(sl) * kPairsAll;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int r = (tid + i * kAtThreads) / (HD / 2);
-            const float mk = __ldcg(p.part_ml + sl * kRows + r).x;
-            const float by = mk == -INFINITY ? 1.f : ex2(mk - s_M[r]);
-            const float2 y = __ldcg(src + tid + i * kAtThreads);
-            x[i].x = fmaf(y.x, by, x[i].x);
-            x[i].y = fmaf(y.y, by, x[i].y);
-          }
-        }
-        if (out) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) finish(tid + i * kAtThreads, x[i], s_L[(tid + i * kAtThreads) / (HD / 2)]);
-        } else {
-          float2 *o = reinterpret_cast<float2 *>(p.part) + static_cast<long long>(slot_of(b0)) * kPairsAll;
-          __syncthreads();  // every thread has read b0's reference
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) __stcg(o + tid + i * kAtThreads, x[i]);
-          if (tid < kRows) __stcg(p.part_ml + slot_of(b0) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
-        }
-      };
-      // arrives at a counter of `n`; true in every thread of the block that is last
-      auto arrive = [&](uint32_t *counter, uint32_t n) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const uint32_t old = atomicAdd(counter, 1u);
-          s_last = old == n - 1;
-          if (old == n - 1) *counter = 0;  // for the next call
-          __threadfence();
-        }
-        __syncthreads();
-        return s_last != 0;
-      };
-      const int n = last - first + 1;
-      if (n <= kJoin) {
-        if (arrive(p.count + first, n)) join(first, last, 1, true);
-      } else {
-        const int lead = first + (me - first) / kJoin * kJoin, end = min(last, lead + kJoin - 1);
-        if (arrive(p.count + gridDim.x + slot_of(lead), end - lead + 1)) {
-          join(lead, end, 1, false);
-          if (arrive(p.count + first, (n + kJoin - 1) / kJoin)) join(first, last, kJoin, true);
+    if (s_bad) {  // values of this segment that are not finite and that only some rows see
+      const int p1 = min(len, seg1 * kUnit);
+#pragma unroll 1
+      for (int q = max(static_cast<int>(max(all_see + 1, 0ll)), seg0 * kUnit); q < p1; ++q) {
+        const int r = row_of(q);
+        if (r < 0) continue;
+#pragma unroll 1
+        for (int i = tid; i < kRows * HD; i += kAtThreads) {
+          const long long o = static_cast<long long>(r) * HD + i % HD;
+          bool bad;
+          if constexpr (E4M3) bad = (static_cast<const uint8_t *>(a.kv.v)[o] & 0x7f) == 0x7f;
+          else bad = (static_cast<const uint16_t *>(a.kv.v)[o] & 0x7f80) == 0x7f80;
+          if (bad && q <= s_lim[i / HD]) merge[i / HD * kLd + i % HD] = __uint_as_float(0x7fffffffu);
         }
       }
+      __syncthreads();
     }
-    u = at + seg1;
+    auto finish = [&](int i, float4 x, float L) {
+      const int r = i / kRowPieces;
+      if (s_out[r] < 0) return;
+      const bool none = s_lim[r] < 0 || L == 0.f;
+      const float by = 1.0f / L;
+      x = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * by, x.y * by, x.z * by, x.w * by);
+      const long long o = s_out[r] + 4 * (i % kRowPieces);
+      if constexpr (sizeof(TIO) == 4) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = x;
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + o) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+      }
+    };
+    if (whole) {
+#pragma unroll 1
+      for (int i = tid; i < kPieces; i += kAtThreads) finish(i, summed(i), s_L[i / kRowPieces]);
+    } else {
+      // ---- this block's part of the item, and the join by the last to leave one ------------
+      // block i of one-weight shares holds weight i
+      const bool single = place.share == 1 && place.more == 0;
+      const int first = single ? static_cast<int>(at) : block_of(at, place.share, place.more);
+      const int last = single ? static_cast<int>(at) + weight - 1 : block_of(at + weight - 1, place.share, place.more);
+      const int me = blockIdx.x;
+      // slot 1: the item begins in this block; slot 0: it began before
+      auto slot_of = [&](int blk) { return 2 * blk + (blk == first); };
+#pragma unroll 1
+      for (int i = tid; i < kPieces; i += kAtThreads) __stcg(p.part + static_cast<long long>(slot_of(me)) * kPieces + i, summed(i));
+      if (tid < kRows) __stcg(p.part_ml + slot_of(me) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
+      // The parts of up to kJoin blocks b0, b0 + step, .. are joined by the last of them
+      // to arrive at their counter: into the output, or, of an item in more blocks,
+      // first in groups, back into the part of each group's first block.
+      const int n_parts = last - first + 1;
+      int b0 = first, parts = n_parts, step = 1;
+      uint32_t *counter = p.count + first;
+      if (n_parts > kJoin) {
+        b0 = first + (me - first) / kJoin * kJoin;
+        parts = min(last - b0 + 1, kJoin);
+        counter = p.count + kAtMaxBlocks + slot_of(b0);
+      }
+#pragma unroll 1
+      for (;;) {
+        __syncthreads();  // the block's part is written; the release below makes it seen
+        if (tid == 0) {
+          uint32_t old;
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+          s_last = old == static_cast<uint32_t>(parts - 1);
+          if (s_last) *counter = 0;  // for the next call
+        }
+        __syncthreads();
+        if (!s_last) break;
+        const bool final = n_parts <= kJoin || step > 1;
+#pragma unroll 1
+        for (int i = tid; i < kPieces; i += kAtThreads) {
+          const int r = i / kRowPieces;
+          float M = -INFINITY, L = 0.f;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int k0 = 0; k0 < parts; k0 += 8) {
+            float4 y[8];
+            float2 ml[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {  // behind the last part: the last again, without weight
+              const int slot = slot_of(b0 + min(k0 + k, parts - 1) * step);
+              ml[k] = __ldcg(p.part_ml + slot * kRows + r);
+              y[k] = __ldcg(p.part + static_cast<long long>(slot) * kPieces + i);
+            }
+            float to = M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to = fmaxf(to, ml[k].x);
+            const float old = to == -INFINITY ? 1.f : ex2(M - to);
+            M = to;
+            L *= old;
+            x.x *= old;
+            x.y *= old;
+            x.z *= old;
+            x.w *= old;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k0 + k < parts) {
+                const float by = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - M);
+                L = fmaf(ml[k].y, by, L);
+                x.x = fmaf(y[k].x, by, x.x);
+                x.y = fmaf(y[k].y, by, x.y);
+                x.z = fmaf(y[k].z, by, x.z);
+                x.w = fmaf(y[k].w, by, x.w);
+              }
+          }
+          if (final) {
+            finish(i, x, L);
+          } else {
+            __stcg(p.part + static_cast<long long>(slot_of(b0)) * kPieces + i, x);  // read by this thread alone
+            if (i % kRowPieces == 0) {
+              s_M[r] = M;
+              s_L[r] = L;
+            }
+          }
+        }
+        if (final) break;
+        __syncthreads();  // every thread has read b0's reference
+        if (tid < kRows) __stcg(p.part_ml + slot_of(b0) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
+        b0 = first;
+        step = kJoin;
+        parts = (n_parts + kJoin - 1) / kJoin;
+        counter = p.count + first;
+      }
+    }
+    u = at + w1;
   }
 }
 
@@ -1060,24 +1161,26 @@ cudaError_t launch_kv_gather(const KvGather &a, int out_dtype, cudaStream_t st) 
               : launch(kv_gather<128, __nv_bfloat16, false>, grid, block, 0, st, a);
 }
 
-// Workspace: counters (three words per block), then the parts of at most two items per
-// block; laid out for the largest grid and the most rows, whatever a call takes.
-static size_t count_bytes(int n_sm) { return (sizeof(uint32_t) * 3 * kAtMaxBlocks * static_cast<size_t>(n_sm) + 255) / 256 * 256; }
+// Workspace: counters (one per block, two per block for the first level of a join), then
+// the parts of at most two items per block, laid out for the most rows.
+constexpr size_t kCountBytes = sizeof(uint32_t) * 3 * kAtMaxBlocks;
 
 size_t paged_attention_workspace(int n_sm) {
-  // 2 blocks per SM x 2 parts x 32 rows are more than 3 x 2 x 8 and 2 x 2 x 16
-  return count_bytes(n_sm) + sizeof(float) * 2 * 2 * static_cast<size_t>(n_sm) * 32 * (128 + 2);
+  // two parts of 32 rows in 2 blocks per SM: more than 3 blocks of 8 rows or 2 of 16
+  return kCountBytes + sizeof(float) * 2 * 2 * static_cast<size_t>(n_sm) * 32 * (128 + 2);
 }
 
 template <int HD, typename TIO, bool E4M3, int NT>
 static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStream_t st) {
   using S = AtShape<HD, TIO, E4M3, NT>;
-  static_assert(S::kBlocks * S::kRows * 2 <= 2 * 2 * 32 && S::kBlocks <= kAtMaxBlocks, "workspace");
-  const int blocks = n_sm * S::kBlocks;
+  static_assert(S::kBlocks * S::kRows <= 2 * 32 && HD <= 128, "workspace");
+  const int blocks = std::min(n_sm * S::kBlocks, kAtMaxBlocks);
   p.n_rg = (p.R + S::kRows - 1) / S::kRows;
+  p.few = p.a.B <= 32 && p.n_rg == 1 &&
+          static_cast<long long>(p.a.B) * p.a.kv.n_kv_heads * (p.cap / kUnit + 1) < (1ll << 31);
   p.count = static_cast<uint32_t *>(workspace);
-  p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + count_bytes(n_sm));
-  p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD);
+  p.part = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + kCountBytes);
+  p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD / 4);
   if (S::kSmem > 46 * 1024) {
     static std::atomic<uint64_t> done{0};  // devices on which the size is set
     int dev = 0;
@@ -1089,7 +1192,7 @@ static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStr
       if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
     }
   }
-  return launch(paged_attn<HD, TIO, E4M3, NT>, dim3(blocks), dim3(kAtThreads), S::kSmem, st, p);
+  return launch(paged_attn<HD, TIO, E4M3, NT>, dim3(blocks), dim3(S::kThreads), S::kSmem, st, p);
 }
 
 template <int HD, typename TIO, bool E4M3>
@@ -1099,16 +1202,19 @@ static cudaError_t run_rows(AttnArgs &p, void *workspace, int n_sm, cudaStream_t
   return run_attention<HD, TIO, E4M3, 4>(p, workspace, n_sm, st);
 }
 
+static Div div_by(uint32_t d) {  // d < 2^31: exact for dividends below 2^31 (Granlund and Montgomery 1994)
+  uint32_t l = 0;
+  while ((1u << l) < d) ++l;
+  return {static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 cudaError_t launch_paged_attention(const PagedAttn &a, int dtype, void *workspace, int n_sm, cudaStream_t st) {
   AttnArgs p{};
   p.a = a;
   p.G = a.Hq / a.kv.n_kv_heads;
   p.R = a.T * p.G;
-  const uint32_t d = a.kv.page_size;
-  uint32_t l = 0;
-  while ((1u << l) < d) ++l;  // d < 2^31
-  p.shift = 31 + l;
-  p.magic = static_cast<uint32_t>(((1ull << p.shift) + d - 1) / d);
+  p.by_page = div_by(a.kv.page_size);
+  p.by_G = div_by(p.G);
   p.cap = a.kv.max_pages * a.kv.page_size;
   p.qscale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);  // log2(e)
   const bool f32 = dtype == MK_F32, e4m3 = a.kv.dtype == MK_E4M3;

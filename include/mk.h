@@ -412,7 +412,8 @@ MK_API uint64_t mk_paged_attention_workspace(void);
  *   scale      : finite, e.g. 1 / sqrt(head_dim)
  *   rope       : as mk_kv_append, applied to q at its row's position; or NULL.  A row
  *                at or past rope_len gives zeros
- *   out        : device [B][T][n_q_heads][head_dim] of `dtype`, contiguous
+ *   out        : device [B][T][n_q_heads][head_dim] of `dtype`, contiguous, 16-byte
+ *                aligned
  *   workspace  : see mk_paged_attention_workspace; 16-byte aligned
  * Scores, softmax statistics and sums are fp32.  The result does not depend on
  * which block finishes first.  One launch; asynchronous.  Errors: MK_ERR_ARG,

@@ -82,7 +82,7 @@ def test_rope_refusals(call, kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(q=None), mk.MK_ERR_ARG), (dict(out=None), mk.MK_ERR_ARG), (dict(hq=3), mk.MK_ERR_ARG),
+    (dict(q=None), mk.MK_ERR_ARG), (dict(out=None), mk.MK_ERR_ARG), (dict(out=PTR + 8), mk.MK_ERR_ARG), (dict(hq=3), mk.MK_ERR_ARG),
     (dict(hq=0), mk.MK_ERR_ARG), (dict(scale=float("inf")), mk.MK_ERR_ARG), (dict(scale=float("nan")), mk.MK_ERR_ARG),
     (dict(ws=None), mk.MK_ERR_ARG), (dict(ws=PTR + 4), mk.MK_ERR_ARG),
     (dict(T=1 << 20, hq=1 << 10), mk.MK_ERR_UNSUPPORTED)])
