@@ -1022,6 +1022,7 @@ MK_API int mk_paged_attention(const mk_paged_kv *kv, const void *q, mk_strides q
   a.B = B; a.T = T; a.scale = scale;
   a.rope = reinterpret_cast<const float2 *>(rope); a.rope_len = rope_len;
   a.out = out;
+  a.vec = vec_ok(q, qs, dtype);
   CUDA_TRY(launch_paged_attention(a, dtype, workspace, n_sm, static_cast<cudaStream_t>(stream)));
   return MK_OK;
 }

@@ -255,7 +255,8 @@ struct KvAppend {
   int B, T;
   const float2 *rope;
   int rope_len;
-  int vec;  // operands allow 16-byte accesses
+  int vec;     // operands allow 16-byte accesses
+  int spread;  // groups of lanes per token (set by the launch)
 };
 cudaError_t launch_kv_append(const KvAppend &a, int in_dtype, cudaStream_t st);
 
@@ -265,7 +266,7 @@ struct KvGather {
   int B, T;
   void *k, *v;
   mk_strides ks, vs;
-  int vec;
+  int vec, spread;
 };
 cudaError_t launch_kv_gather(const KvGather &a, int out_dtype, cudaStream_t st);
 
@@ -280,6 +281,7 @@ struct PagedAttn {
   const float2 *rope;
   int rope_len;
   void *out;
+  int vec;  // rows of q start on 16-byte boundaries
 };
 size_t paged_attention_workspace(int n_sm);
 cudaError_t launch_paged_attention(const PagedAttn &a, int dtype, void *workspace, int n_sm, cudaStream_t st);

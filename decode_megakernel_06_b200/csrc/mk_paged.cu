@@ -40,40 +40,12 @@ __device__ __forceinline__ int pool_row(const mk_paged_kv &kv, int b, int h, lon
   return (page * kv.n_kv_heads + h) * kv.page_size + static_cast<int>(p - e * kv.page_size);
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// Eight consecutive values as fp32: 16-byte loads where the operand allows them.
-__device__ __forceinline__ void load8(const float *p, int vec, float (&x)[8]) {
-  if (vec) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p[i];
-  }
-}
-
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int vec, float (&x)[8]) {
-  if (vec) {
-    unpack8(*reinterpret_cast<const uint4 *>(p), x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
   }
 }
 
@@ -119,127 +91,205 @@ __device__ __forceinline__ void decode8(const uint2 &u, float (&x)[8]) {
   }
 }
 
-// Rotate-half of a row held 8 values a lane: value i pairs with i + HD / 2, which
-// the lane HD / 16 away holds.  cs: the position's (cos, sin) of the HD / 2 angles.
-template <int HD>
-__device__ __forceinline__ void rotate8(float (&x)[8], const float2 *cs, int lane8) {
+// ---------------------------------------------------------------------------
+// Append.  A group of HD / 8 lanes takes a token of sequence blockIdx.y and every
+// `spread`-th of its KV heads: the place of the token is looked up once, its
+// rotary angles are held in registers, and the loads of several heads' rows are in
+// flight together.  A key row is rotated in fp32; then each value is rounded once:
+// to bf16, or to the e4m3 code of x / scale with scale = max(amax / 448, 2^-126)
+// over the row's finite values (half a step of e4m3, 2^-4 relative; the division
+// keeps x = amax on the largest code).  Every lane of a warp stays in the shuffles;
+// rows without a place are not written.  Bound by memory: each input byte is read
+// once, each cache byte written once.
+// ---------------------------------------------------------------------------
+constexpr int kHeadsAtOnce = 2;  // heads whose key and value rows a group loads together
+
+// Eight values of a row in their own type.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p, int vec) {
+    if (vec) {
+      a = *reinterpret_cast<const float4 *>(p);
+      b = *reinterpret_cast<const float4 *>(p + 4);
+    } else {
+      a = make_float4(p[0], p[1], p[2], p[3]);
+      b = make_float4(p[4], p[5], p[6], p[7]);
+    }
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int vec) {
+    if (vec) {
+      u = *reinterpret_cast<const uint4 *>(p);
+    } else {
+      const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+      u = make_uint4(q[0] | static_cast<uint32_t>(q[1]) << 16, q[2] | static_cast<uint32_t>(q[3]) << 16,
+                     q[4] | static_cast<uint32_t>(q[5]) << 16, q[6] | static_cast<uint32_t>(q[7]) << 16);
+    }
+  }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8(u, x); }
+};
+
+// Rounds a row's eight values of this lane and writes them to row `row` of a pool.
+template <int HD, bool E4M3>
+__device__ __forceinline__ void put_row(void *pool, float *scales, long long row, bool on, const float (&x)[8], int lane8) {
   constexpr int kLanes = HD / 8;
-  const bool low = lane8 < kLanes / 2;
-  const float2 *c = cs + 8 * (lane8 % (kLanes / 2));
+  const long long at = row * HD + 8 * lane8;
+  if constexpr (E4M3) {
+    float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float other = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2, kLanes);
-    const float2 w = c[i];
-    x[i] = low ? x[i] * w.x - other * w.y : x[i] * w.x + other * w.y;
+    for (int i = 0; i < 8; ++i) {
+      const float m = fabsf(x[i]);
+      amax = m < INFINITY ? fmaxf(amax, m) : amax;  // NaN compares false
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
+    const float scale = fmaxf(amax / kE4m3Max, kTinyScale);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] / scale, x[2 * i + 1] / scale),
+                                                              __NV_SATFINITE, __NV_E4M3);
+      w[i / 2] |= static_cast<uint32_t>(c) << (16 * (i & 1));
+    }
+    if (on) {
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = make_uint2(w[0], w[1]);
+      if (lane8 == 0) scales[row] = scale;
+    }
+  } else if (on) {
+    store8(static_cast<__nv_bfloat16 *>(pool) + at, 1, x);
   }
 }
 
-// ---------------------------------------------------------------------------
-// Append.  Items are (t, head, key or value) rows of sequence blockIdx.y, the
-// heads fastest, one group of HD / 8 lanes each.  A key row is rotated in fp32;
-// then each value is rounded once: to bf16, or to the e4m3 code of x / scale with
-// scale = max(amax / 448, 2^-126) over the row's finite values (half a step of
-// e4m3, 2^-4 relative; the division keeps x = amax on the largest code).  Every
-// lane of a warp stays in the shuffles; rows without a place are not written.
-// Bound by memory: each input byte is read once, each cache byte written once.
-// ---------------------------------------------------------------------------
 template <int HD, typename TIn, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) kv_append(const __grid_constant__ KvAppend a) {
   pdl_wait();
   pdl_launch();
   constexpr int kLanes = HD / 8;
-  const int lane8 = threadIdx.x % kLanes;
-  const int rows = a.T * a.kv.n_kv_heads * 2;
-  const int item = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;
-  const int is_v = item < rows ? item % 2 : 0;
-  const int h = item / 2 % a.kv.n_kv_heads, t = item / 2 / a.kv.n_kv_heads;
+  const int lane8 = threadIdx.x % kLanes, hkv = a.kv.n_kv_heads;
+  const int group = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;
+  const int t = group / a.spread, h0 = group - t * a.spread;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     const long long p = static_cast<long long>(a.positions[b]) + t;
-    bool on = item < rows && (!a.counts || t < a.counts[b]) && (!a.rope || p < a.rope_len);
-    const int row = on ? pool_row(a.kv, b, h, p) : -1;
-    on = row >= 0;
-    float x[8];
+    bool on = t < a.T && (!a.counts || t < a.counts[b]) && (!a.rope || p < a.rope_len);
+    const int first = on ? pool_row(a.kv, b, 0, p) : -1;  // the row of head 0
+    on = first >= 0;
+    if (!__any_sync(0xffffffffu, on)) continue;
+    float2 cs[8];
+    if (a.rope) {
+      const float2 *src = a.rope + (on ? p * (HD / 2) : 0) + 8 * (lane8 % (kLanes / 2));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (on) {
-      const mk_strides &s = is_v ? a.vs : a.ks;
-      const TIn *src = static_cast<const TIn *>(is_v ? a.v : a.k) + b * s.seq + t * s.token + h * s.head;
-      load8(src + 8 * lane8, a.vec, x);
-    }
-    if (a.rope) {  // the shuffles run in every lane
-      float r[8];
+      for (int i = 0; i < 8; ++i) cs[i] = src[i];
+      if (lane8 < kLanes / 2) {  // the sine's sign of a row's lower half
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = x[i];
-      rotate8<HD>(r, a.rope + (on ? p * (HD / 2) : 0), lane8);
-      if (!is_v) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = r[i];
+        for (int i = 0; i < 8; ++i) cs[i].y = -cs[i].y;
       }
     }
-    void *pool = is_v ? a.kv.v : a.kv.k;
-    const long long at = static_cast<long long>(row) * HD + 8 * lane8;
-    if constexpr (E4M3) {
-      float amax = 0.f;
+    const TIn *k = static_cast<const TIn *>(a.k) + b * a.ks.seq + t * a.ks.token + 8 * lane8;
+    const TIn *v = static_cast<const TIn *>(a.v) + b * a.vs.seq + t * a.vs.token + 8 * lane8;
+    for (int hb = 0; hb < hkv; hb += kHeadsAtOnce * a.spread) {  // as often in every lane
+      Eight<TIn> rk[kHeadsAtOnce], rv[kHeadsAtOnce];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(x[i]);
-        amax = m < INFINITY ? fmaxf(amax, m) : amax;  // NaN compares false
+      for (int i = 0; i < kHeadsAtOnce; ++i) {
+        const int h = hb + h0 + i * a.spread;
+        rk[i].clear();
+        rv[i].clear();
+        if (on && h < hkv) {
+          rk[i].load(k + h * a.ks.head, a.vec);
+          rv[i].load(v + h * a.vs.head, a.vec);
+        }
       }
 #pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
-      const float scale = fmaxf(amax / kE4m3Max, kTinyScale);
-      uint32_t w[2] = {0, 0};
+      for (int i = 0; i < kHeadsAtOnce; ++i) {
+        const int h = hb + h0 + i * a.spread;
+        if (!__any_sync(0xffffffffu, h < hkv)) break;
+        const bool put = on && h < hkv;
+        const long long row = first + static_cast<long long>(h) * a.kv.page_size;
+        float x[8];
+        rk[i].get(x);
+        if (a.rope) {  // value j turns with j + HD / 2, which the lane HD / 16 away holds
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] / scale, x[2 * i + 1] / scale),
-                                                                __NV_SATFINITE, __NV_E4M3);
-        w[i / 2] |= static_cast<uint32_t>(c) << (16 * (i & 1));
+          for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, x[j], kLanes / 2, kLanes);
+            x[j] = x[j] * cs[j].x + other * cs[j].y;
+          }
+        }
+        put_row<HD, E4M3>(a.kv.k, a.kv.k_scale, row, put, x, lane8);
+        rv[i].get(x);
+        put_row<HD, E4M3>(a.kv.v, a.kv.v_scale, row, put, x, lane8);
       }
-      if (on) {
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = make_uint2(w[0], w[1]);
-        if (lane8 == 0) (is_v ? a.kv.v_scale : a.kv.k_scale)[row] = scale;
-      }
-    } else if (on) {
-      store8(static_cast<__nv_bfloat16 *>(pool) + at, 1, x);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Gather.  Items as in append; value = code * scale in fp32, rounded once to the
-// output's type; zeros for positions without a place.
+// Gather.  Groups of lanes and heads as in append; value = code * scale in fp32,
+// rounded once to the output's type; zeros for positions without a place.
 // ---------------------------------------------------------------------------
 template <int HD, typename TOut, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) kv_gather(const __grid_constant__ KvGather a) {
   pdl_wait();
   pdl_launch();
-  constexpr int kLanes = HD / 8;
-  const int lane8 = threadIdx.x % kLanes;
-  const int rows = a.T * a.kv.n_kv_heads * 2;
-  const int item = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;
-  if (item >= rows) return;
-  const int is_v = item % 2, h = item / 2 % a.kv.n_kv_heads, t = item / 2 / a.kv.n_kv_heads;
+  constexpr int kLanes = HD / 8, kWords = E4M3 ? 2 : 4;
+  const int lane8 = threadIdx.x % kLanes, hkv = a.kv.n_kv_heads;
+  const int group = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;
+  const int t = group / a.spread, h0 = group - t * a.spread;
+  if (t >= a.T) return;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     if (a.counts && t >= a.counts[b]) continue;
-    const int row = pool_row(a.kv, b, h, static_cast<long long>(a.starts[b]) + t);
-    float x[8];
+    const int first = pool_row(a.kv, b, 0, static_cast<long long>(a.starts[b]) + t);
+    TOut *ko = static_cast<TOut *>(a.k) + b * a.ks.seq + t * a.ks.token + 8 * lane8;
+    TOut *vo = static_cast<TOut *>(a.v) + b * a.vs.seq + t * a.vs.token + 8 * lane8;
+    for (int hb = 0; hb < hkv; hb += kHeadsAtOnce * a.spread) {  // as often in every lane
+      uint32_t raw[kHeadsAtOnce][2][kWords];
+      float scale[kHeadsAtOnce][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (row >= 0) {
-      const void *pool = is_v ? a.kv.v : a.kv.k;
-      const long long at = static_cast<long long>(row) * HD + 8 * lane8;
-      if constexpr (E4M3) {
-        decode8(*reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + at), x);
-        const float s = (is_v ? a.kv.v_scale : a.kv.k_scale)[row];
+      for (int i = 0; i < kHeadsAtOnce; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= s;
-      } else {
-        load8(static_cast<const __nv_bfloat16 *>(pool) + at, 1, x);
+        for (int kv = 0; kv < 2; ++kv) {
+          const int h = hb + h0 + i * a.spread;
+          const bool on = first >= 0 && h < hkv;
+          const long long row = first + static_cast<long long>(h) * a.kv.page_size;
+          const char *src = static_cast<const char *>(kv ? a.kv.v : a.kv.k) + (row * HD + 8 * lane8) * (kWords / 2);
+          scale[i][kv] = 1.f;
+          if constexpr (E4M3) {
+            const uint2 u = on ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
+            raw[i][kv][0] = u.x; raw[i][kv][1] = u.y;
+            if (on) scale[i][kv] = (kv ? a.kv.v_scale : a.kv.k_scale)[row];
+          } else {
+            const uint4 u = on ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+            raw[i][kv][0] = u.x; raw[i][kv][1] = u.y; raw[i][kv][2] = u.z; raw[i][kv][3] = u.w;
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < kHeadsAtOnce; ++i) {
+        const int h = hb + h0 + i * a.spread;
+        if (h >= hkv) break;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          float x[8];
+          if constexpr (E4M3) {
+            decode8(make_uint2(raw[i][kv][0], raw[i][kv][1]), x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= scale[i][kv];
+          } else {
+            unpack8(make_uint4(raw[i][kv][0], raw[i][kv][1], raw[i][kv][2], raw[i][kv][3]), x);
+          }
+          store8((kv ? vo + h * a.vs.head : ko + h * a.ks.head), a.vec, x);
+        }
       }
     }
-    const mk_strides &s = is_v ? a.vs : a.ks;
-    TOut *dst = static_cast<TOut *>(is_v ? a.v : a.k) + b * s.seq + t * s.token + h * s.head;
-    store8(dst + 8 * lane8, a.vec, x);
   }
 }
 
@@ -305,16 +355,52 @@ struct Geo {
 template <int HD, typename TIO, bool E4M3, int NT>
 struct AtShape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = 4;
+  // Resident warps per SM are what registers allow.  With one tile of rows as small
+  // blocks, which leave fewer items cut and overlap one's prologue with another's
+  // loop (27 us against 34 in blocks of 12 warps, 32 ragged sequences); with more
+  // rows in one block, whose join has half as many parts and twice the threads.
+  static constexpr int kWarps = NT == 1 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kBlocks = NT == 1 ? 3 : 2;   // resident per SM: what registers allow
+  static constexpr int kBlocks = NT == 1 ? 3 : 1;
   static constexpr int NQ = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int NP = sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int kQBytes = Geo<HD, E4M3>::KS * NQ * NT * 32 * 8;      // fragments of Q^T
-  static constexpr int kStage = kRows * HD * 4;                             // rotated q, fp32
+  static constexpr int kLdq = HD + 4;                                       // row stride of the rotated q
+  static constexpr int kStage = kRows * kLdq * 4;
   static constexpr int kLd = HD + 4;                                        // row stride of the warps' sums
   static constexpr int kMerge = kWarps * kRows * kLd * 4;
   static constexpr int kSmem = kMerge > kQBytes + kStage ? kMerge : kQBytes + kStage;
+};
+
+// Four consecutive values of a row, kept in their own type until they are used.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 v;
+  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float *p, int vec) {
+    if (vec) v = *reinterpret_cast<const float4 *>(p);
+    else v = make_float4(p[0], p[1], p[2], p[3]);
+  }
+  __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void clear() { v = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int vec) {
+    if (vec) {
+      v = *reinterpret_cast<const uint2 *>(p);
+    } else {
+      const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+      v = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
 };
 
 struct Div {  // x / d = (x magic) >> shift for 0 <= x < 2^31
@@ -327,6 +413,7 @@ struct Div {  // x / d = (x magic) >> shift for 0 <= x < 2^31
 struct AttnArgs {
   PagedAttn a;
   int G, R, n_rg;            // query heads of a KV head, rows of a KV head, row groups
+  int vec;                   // rows of q start on 16-byte boundaries
   int few;                   // up to 32 sequences of one row group each, units below 2^31
   Div by_page, by_G;
   int cap;                   // positions of a page table's row
@@ -562,7 +649,7 @@ __global__ void __launch_bounds__((AtShape<HD, TIO, E4M3, NT>::kThreads), (AtSha
 paged_attn(const __grid_constant__ AttnArgs p) {
   using S = AtShape<HD, TIO, E4M3, NT>;
   using X = Geo<HD, E4M3>;
-  constexpr int kRows = S::kRows, NQ = S::NQ, NP = S::NP, KS = X::KS, KW = X::KW, VW = X::VW, kLd = S::kLd,
+  constexpr int kRows = S::kRows, NQ = S::NQ, NP = S::NP, KS = X::KS, KW = X::KW, VW = X::VW, kLd = S::kLd, kLdq = S::kLdq,
                 kAtWarps = S::kWarps, kAtThreads = S::kThreads;
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ long long s_scan[kAtWarps + 2];
@@ -663,72 +750,83 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 
     // ---- Q: rotated, in pieces, in the layout of the product's B operand -----------------
     {
-      constexpr int kPerRow = kAtThreads / kRows, kPairs = HD / 2 / kPerRow;
-      const int r = tid / kPerRow, part = tid % kPerRow;  // pairs part, part + kPerRow, .. of row r
+      // lanes part, part + kPerRow, .. of a row hold four pairs of dimensions each
+      constexpr int kPerRow = kAtThreads / kRows < HD / 8 ? kAtThreads / kRows : HD / 8, kQuads = HD / 8 / kPerRow;
+      const int r = tid / kPerRow, part = tid % kPerRow;
+      const bool lane_on = r < kRows;  // HD = 64 leaves half of the threads without a piece
       const int t = p.by_G.of(r0 + r), hq = h * p.G + (r0 + r) - t * p.G;
       const long long at_p = static_cast<long long>(pos) + t;
-      const bool is_row = r0 + r < p.R && t < n_rows;
+      const bool is_row = lane_on && r0 + r < p.R && t < n_rows;
       const bool on = is_row && at_p >= 0 && (!a.rope || at_p < a.rope_len);
-      const TIO *q = static_cast<const TIO *>(a.q) + b * a.qs.seq + t * a.qs.token + hq * a.qs.head + part;
-      const float2 *cs = a.rope + at_p * (HD / 2) + part;
-      const bool turn = a.rope && on;
-      TIO lo[kPairs], hi[kPairs];
-      float2 w[kPairs];
+      const TIO *q = static_cast<const TIO *>(a.q) + b * a.qs.seq + t * a.qs.token + hq * a.qs.head + 4 * part;
+      const float2 *cs = a.rope + at_p * (HD / 2) + 4 * part;
+      Four<TIO> lo[kQuads], hi[kQuads];
+      float2 w[kQuads][4];
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        lo[i] = on ? q[kPerRow * i] : TIO(0.f);
-        hi[i] = on ? q[kPerRow * i + HD / 2] : TIO(0.f);
-        w[i] = turn ? cs[kPerRow * i] : make_float2(1.f, 0.f);
+      for (int i = 0; i < kQuads; ++i) {
+        lo[i].clear();
+        hi[i].clear();
+        if (on) {
+          lo[i].load(q + 4 * kPerRow * i, p.vec);
+          hi[i].load(q + 4 * kPerRow * i + HD / 2, p.vec);
+          if (a.rope) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i][j] = cs[4 * kPerRow * i + j];
+          }
+        }
       }
       load_k(row);  // the first unit's loads wait for its page's number; the rows' are on their way
       load_v(row);
-      float x[kPairs], y[kPairs];
+      float x[kQuads][4], y[kQuads][4];
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        x[i] = to_f(lo[i]) * w[i].x - to_f(hi[i]) * w[i].y;
-        y[i] = to_f(hi[i]) * w[i].x + to_f(lo[i]) * w[i].y;
-      }
-      if (!a.rope) {  // exactly the row, infinities too
+      for (int i = 0; i < kQuads; ++i)
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          x[i] = to_f(lo[i]);
-          y[i] = to_f(hi[i]);
+        for (int j = 0; j < 4; ++j) {
+          const float u = lo[i].at(j), v = hi[i].at(j);
+          x[i][j] = a.rope && on ? u * w[i][j].x - v * w[i][j].y : u;
+          y[i][j] = a.rope && on ? v * w[i][j].x + u * w[i][j].y : v;
         }
-      }
       float f = p.qscale;
       if constexpr (E4M3) {  // a power of two takes the row's largest value to [2^10, 2^11)
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(x[i][j]), fabsf(y[i][j])));
 #pragma unroll
         for (int o = kPerRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int e = m < INFINITY ? max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) : 0;
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23);
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          x[i] *= up;
-          y[i] *= up;
-        }
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[i][j] *= up;
+            y[i][j] *= up;
+          }
         f *= __uint_as_float(static_cast<uint32_t>(127 + e - 10) << 23);
       }
       __syncthreads();  // the last item's shared memory is free
+      if (lane_on) {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        stage[r * HD + part + kPerRow * i] = x[i];
-        stage[r * HD + part + kPerRow * i + HD / 2] = y[i];
-      }
-      if (part == 0) {
-        s_f[r] = f;
-        s_lim[r] = on ? static_cast<int>(min(at_p, 0x7fffffffll)) : -1;
-        s_out[r] = is_row ? ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * HD : -1;
+        for (int i = 0; i < kQuads; ++i) {
+          float *dst = stage + r * kLdq + 4 * (part + kPerRow * i);
+          *reinterpret_cast<float4 *>(dst) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+          *reinterpret_cast<float4 *>(dst + HD / 2) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
+        }
+        if (part == 0) {
+          s_f[r] = f;
+          s_lim[r] = on ? static_cast<int>(min(at_p, 0x7fffffffll)) : -1;
+          s_out[r] = is_row ? ((static_cast<long long>(b) * a.T + t) * a.Hq + hq) * HD : -1;
+        }
       }
       if (tid == 0) s_bad = 0;
     }
     __syncthreads();
-#pragma unroll 1
+#pragma unroll 2
     for (int i = tid; i < KS * NT * 32; i += kAtThreads) {
       const int l = i % 32, n = i / 32 % NT, ks = i / 32 / NT;
-      const float4 s = *reinterpret_cast<const float4 *>(stage + (8 * n + l / 4) * HD + X::kdim(ks, l % 4));
+      const float4 s = *reinterpret_cast<const float4 *>(stage + (8 * n + l / 4) * kLdq + X::kdim(ks, l % 4));
       uint32_t w0[NQ], w1[NQ];
       if constexpr (E4M3) {
         split_f16(s.x, s.y, w0);
@@ -1123,16 +1221,21 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-dim3 row_grid(const mk_paged_kv &kv, int B, int T) {
+// Groups per token and the grid: heads of a token are spread over groups while
+// there are too few tokens to fill the GPU (about 64 groups of an SM).
+dim3 row_grid(const mk_paged_kv &kv, int B, int T, int &spread) {
   const int per = kRowThreads / (kv.head_dim / 8);
-  const unsigned rows = static_cast<unsigned>(T) * kv.n_kv_heads * 2;  // checked to fit by the caller
-  return dim3((rows + per - 1) / per, std::min(B, 65535));
+  const long long tokens = static_cast<long long>(B) * T, want = 148 * 64;
+  spread = static_cast<int>(std::max(1ll, std::min<long long>(kv.n_kv_heads, want / tokens)));
+  const unsigned groups = static_cast<unsigned>(T) * spread;  // checked to fit by the caller
+  return dim3((groups + per - 1) / per, std::min(B, 65535));
 }
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvAppend &a, int in_dtype, cudaStream_t st) {
-  const dim3 grid = row_grid(a.kv, a.B, a.T), block(kRowThreads);
+cudaError_t launch_kv_append(const KvAppend &args, int in_dtype, cudaStream_t st) {
+  KvAppend a = args;
+  const dim3 grid = row_grid(a.kv, a.B, a.T, a.spread), block(kRowThreads);
   const bool f32 = in_dtype == MK_F32, e4m3 = a.kv.dtype == MK_E4M3;
   if (a.kv.head_dim == 64) {
     if (f32) return e4m3 ? launch(kv_append<64, float, true>, grid, block, 0, st, a)
@@ -1146,8 +1249,9 @@ cudaError_t launch_kv_append(const KvAppend &a, int in_dtype, cudaStream_t st) {
               : launch(kv_append<128, __nv_bfloat16, false>, grid, block, 0, st, a);
 }
 
-cudaError_t launch_kv_gather(const KvGather &a, int out_dtype, cudaStream_t st) {
-  const dim3 grid = row_grid(a.kv, a.B, a.T), block(kRowThreads);
+cudaError_t launch_kv_gather(const KvGather &args, int out_dtype, cudaStream_t st) {
+  KvGather a = args;
+  const dim3 grid = row_grid(a.kv, a.B, a.T, a.spread), block(kRowThreads);
   const bool f32 = out_dtype == MK_F32, e4m3 = a.kv.dtype == MK_E4M3;
   if (a.kv.head_dim == 64) {
     if (f32) return e4m3 ? launch(kv_gather<64, float, true>, grid, block, 0, st, a)
@@ -1166,14 +1270,14 @@ cudaError_t launch_kv_gather(const KvGather &a, int out_dtype, cudaStream_t st) 
 constexpr size_t kCountBytes = sizeof(uint32_t) * 3 * kAtMaxBlocks;
 
 size_t paged_attention_workspace(int n_sm) {
-  // two parts of 32 rows in 2 blocks per SM: more than 3 blocks of 8 rows or 2 of 16
-  return kCountBytes + sizeof(float) * 2 * 2 * static_cast<size_t>(n_sm) * 32 * (128 + 2);
+  // two parts of 32 rows in a block per SM: more than 3 blocks of 8 rows or one of 16
+  return kCountBytes + sizeof(float) * 2 * static_cast<size_t>(n_sm) * 32 * (128 + 2);
 }
 
 template <int HD, typename TIO, bool E4M3, int NT>
 static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStream_t st) {
   using S = AtShape<HD, TIO, E4M3, NT>;
-  static_assert(S::kBlocks * S::kRows <= 2 * 32 && HD <= 128, "workspace");
+  static_assert(S::kBlocks * S::kRows <= 32 && HD <= 128, "workspace");
   const int blocks = std::min(n_sm * S::kBlocks, kAtMaxBlocks);
   p.n_rg = (p.R + S::kRows - 1) / S::kRows;
   p.few = p.a.B <= 32 && p.n_rg == 1 &&
@@ -1213,6 +1317,7 @@ cudaError_t launch_paged_attention(const PagedAttn &a, int dtype, void *workspac
   p.a = a;
   p.G = a.Hq / a.kv.n_kv_heads;
   p.R = a.T * p.G;
+  p.vec = a.vec;
   p.by_page = div_by(a.kv.page_size);
   p.by_G = div_by(p.G);
   p.cap = a.kv.max_pages * a.kv.page_size;
