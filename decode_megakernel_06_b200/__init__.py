@@ -332,15 +332,30 @@ def sample_top_p_phases(logits, temperature: float, top_p: float, uniforms, out_
                                   out_tokens.data_ptr(), stamps.data_ptr(), s.cuda_stream)
 
 
-def _stream_of(device, stream) -> int:
-    """The CUDA stream of a call on ``device``: the given one, which has to be
-    that device's, or its current one."""
+def _call_on(index: int, call, *args) -> int:
+    """call(*args) with device ``index`` current."""
     import torch
 
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"stream: on {s.device}, expected {device}")
-    return s.cuda_stream
+    back = torch.cuda.current_device()
+    if back == index:
+        return call(*args)
+    torch.cuda.set_device(index)
+    try:
+        return call(*args)
+    finally:
+        torch.cuda.set_device(back)
+
+
+def _raw_stream(index: int, stream) -> int:
+    """The CUDA stream of a call on device ``index``: the given one, which has to
+    be that device's, or its current one."""
+    import torch
+
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream: on {stream.device}, expected cuda:{index}")
+    return stream.cuda_stream
 
 
 class PagedKV:
@@ -374,68 +389,73 @@ class PagedKV:
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
         self.desc = mk_paged_kv(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(),
                                 n_pages, page, page_table.shape[1], heads, hd, kinds[k.dtype])
+        self._index, self._batch, self._heads, self._hd = self.device.index, page_table.shape[0], heads, hd
+        self._kinds = {torch.float32: MK_F32, torch.bfloat16: MK_BF16}
+        self._int = torch.int32
 
-    def _rows(self, t, name: str, heads: Optional[int], like=None, written: bool = False):
+    def _rows(self, t, name: str, heads: Optional[int]):
         """Checks a [B, T, heads, head_dim] operand (fp32 or bf16, any strides but a
-        contiguous head_dim); returns (B, T, heads), its strides and its type."""
-        import torch
+        contiguous head_dim); returns its shape, strides and type."""
+        shape, st, kind = t.shape, t.stride(), self._kinds.get(t.dtype)
+        if (kind is None or len(shape) != 4 or shape[3] != self._hd or shape[0] != self._batch or st[3] != 1
+                or (heads is not None and shape[2] != heads) or t.get_device() != self._index):
+            if kind is None:
+                raise ValueError(f"{name}: dtype {t.dtype}, expected float32 or bfloat16")
+            if len(shape) == 4 and shape[3] == self._hd and st[3] != 1:
+                raise ValueError(f"{name}: the head dimension must be contiguous")
+            if t.get_device() != self._index:
+                raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+            raise ValueError(f"{name}: shape {tuple(shape)}, expected [{self._batch}, T, "
+                             f"{'heads' if heads is None else heads}, {self._hd}]")
+        return shape, st, kind
 
-        kinds = {torch.float32: MK_F32, torch.bfloat16: MK_BF16}
-        if t.dtype not in kinds:
-            raise ValueError(f"{name}: dtype {t.dtype}, expected float32 or bfloat16")
-        if t.dim() != 4 or t.shape[3] != self.desc.head_dim or (heads is not None and t.shape[2] != heads):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [B, T, "
-                             f"{'heads' if heads is None else heads}, {self.desc.head_dim}]")
-        if t.shape[0] != self.page_table.shape[0]:
-            raise ValueError(f"{name}: {t.shape[0]} sequences, the page table has {self.page_table.shape[0]}")
-        if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(like.shape)} {like.dtype}")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name}: the head dimension must be contiguous")
-        if written and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-            raise ValueError(f"{name}: written rows must not share memory")
-        if t.device != self.device:
-            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
-        return t.shape[:3], mk_strides(t.stride(0), t.stride(1), t.stride(2)), kinds[t.dtype]
+    def _pair(self, x, y, names: Sequence[str]):
+        """Two such operands of one shape and type: (B, T), the type and both strides."""
+        shape, st, kind = self._rows(x, names[0], self._heads)
+        other, st2, kind2 = self._rows(y, names[1], self._heads)
+        if other != shape or kind2 != kind:
+            raise ValueError(f"{names[1]}: {tuple(other)} {y.dtype}, expected {tuple(shape)} {x.dtype}")
+        return shape[0], shape[1], kind, mk_strides(st[0], st[1], st[2]), mk_strides(st2[0], st2[1], st2[2])
 
-    def _sequences(self, B: int, positions, counts, rope):
-        """Checks the per-sequence operands; returns rope's number of positions."""
-        import torch
+    def _ints(self, t, name: str) -> int:
+        """An int32 operand with an entry per sequence; its pointer."""
+        if t.dtype != self._int or t.numel() < self._batch or not t.is_contiguous() or t.get_device() != self._index:
+            _need(t, self._int, self._batch, name, self.device)
+        return t.data_ptr()
 
-        _need(positions, torch.int32, B, "positions", self.device)
-        if counts is not None:
-            _need(counts, torch.int32, B, "counts", self.device)
+    def _rope(self, rope):
+        """The rotary table's pointer and number of positions (None, 0 without one)."""
         if rope is None:
-            return 0
+            return None, 0
+        import torch
+
         _need(rope, torch.float32, 1, "rope", self.device, dims=3)
-        if tuple(rope.shape[1:]) != (self.desc.head_dim // 2, 2):
-            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, {self.desc.head_dim // 2}, 2]")
-        return rope.shape[0]
+        if rope.shape[1] != self._hd // 2 or rope.shape[2] != 2:
+            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, {self._hd // 2}, 2]")
+        return rope.data_ptr(), rope.shape[0]
 
     def append(self, k, v, positions, counts=None, rope=None, stream=None) -> int:
         """mk_kv_append: rows k, v [B, T, n_kv_heads, head_dim] at positions[b] + t
         (rows t >= counts[b] are not written); with rope, k is rotated first."""
-        import torch
-
-        (B, T, _), ks, kind = self._rows(k, "k", self.desc.n_kv_heads)
-        _, vs, _ = self._rows(v, "v", self.desc.n_kv_heads, like=k)
-        n = self._sequences(B, positions, counts, rope)
-        with torch.cuda.device(self.device):
-            return mk_kv_append(self.desc, k.data_ptr(), ks, v.data_ptr(), vs, kind, positions.data_ptr(),
-                                _ptr(counts), B, T, _ptr(rope), n, _stream_of(self.device, stream))
+        B, T, kind, ks, vs = self._pair(k, v, ("k", "v"))
+        pos = self._ints(positions, "positions")
+        cnt = None if counts is None else self._ints(counts, "counts")
+        table, n = self._rope(rope)
+        return _call_on(self._index, mk_kv_append, self.desc, k.data_ptr(), ks, v.data_ptr(), vs, kind, pos, cnt, B,
+                        T, table, n, _raw_stream(self._index, stream))
 
     def gather(self, starts, out_k, out_v, counts=None, stream=None) -> int:
         """mk_kv_gather: positions starts[b] + t into out_k, out_v
         [B, T, n_kv_heads, head_dim] (any strides, e.g. a contiguous cache
         [B, heads, capacity, head_dim] transposed)."""
-        import torch
-
-        (B, T, _), ks, kind = self._rows(out_k, "out_k", self.desc.n_kv_heads, written=True)
-        _, vs, _ = self._rows(out_v, "out_v", self.desc.n_kv_heads, like=out_k, written=True)
-        self._sequences(B, starts, counts, None)
-        with torch.cuda.device(self.device):
-            return mk_kv_gather(self.desc, starts.data_ptr(), _ptr(counts), B, T, out_k.data_ptr(), ks,
-                                out_v.data_ptr(), vs, kind, _stream_of(self.device, stream))
+        B, T, kind, ks, vs = self._pair(out_k, out_v, ("out_k", "out_v"))
+        for name, s in (("out_k", ks), ("out_v", vs)):
+            if (s.seq == 0 and B > 1) or (s.token == 0 and T > 1) or (s.head == 0 and self._heads > 1):
+                raise ValueError(f"{name}: written rows must not share memory")
+        pos = self._ints(starts, "starts")
+        cnt = None if counts is None else self._ints(counts, "counts")
+        return _call_on(self._index, mk_kv_gather, self.desc, pos, cnt, B, T, out_k.data_ptr(), ks, out_v.data_ptr(),
+                        vs, kind, _raw_stream(self._index, stream))
 
     def attention(self, q, positions, out, workspace, counts=None, scale: Optional[float] = None, rope=None,
                   stream=None) -> int:
@@ -444,18 +464,19 @@ class PagedKV:
         1 / sqrt(head_dim).  ``workspace`` is paged_attention_workspace's."""
         import torch
 
-        (B, T, heads), qs, kind = self._rows(q, "q", None)
+        shape, st, kind = self._rows(q, "q", None)
         _need(out, q.dtype, 1, "out", self.device, dims=4)
-        if out.shape != q.shape:
-            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-        n = self._sequences(B, positions, counts, rope)
+        if out.shape != shape:
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(shape)}")
+        pos = self._ints(positions, "positions")
+        cnt = None if counts is None else self._ints(counts, "counts")
+        table, n = self._rope(rope)
         _need(workspace, torch.uint8, 1, "workspace", self.device)
         if scale is None:
-            scale = self.desc.head_dim ** -0.5
-        with torch.cuda.device(self.device):
-            return mk_paged_attention(self.desc, q.data_ptr(), qs, kind, heads, positions.data_ptr(), _ptr(counts),
-                                      B, T, scale, _ptr(rope), n, out.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel(), _stream_of(self.device, stream))
+            scale = self._hd ** -0.5
+        return _call_on(self._index, mk_paged_attention, self.desc, q.data_ptr(), mk_strides(st[0], st[1], st[2]),
+                        kind, shape[2], pos, cnt, shape[0], shape[1], scale, table, n, out.data_ptr(),
+                        workspace.data_ptr(), workspace.numel(), _raw_stream(self._index, stream))
 
 
 def paged_attention_workspace(device):
@@ -502,11 +523,9 @@ def verify_sample(logits, tokens, temperature: float, top_p: float, uniforms, ou
     _need(out_tokens, torch.int32, B * T, "out_tokens", dev)
     _need(out_accepted, torch.int32, B, "out_accepted", dev)
     _need(workspace, torch.uint8, 1, "workspace", dev)
-    with torch.cuda.device(dev):
-        return mk_verify_sample(logits.data_ptr(), _ptr(draft_logits) if T > 1 else None, tokens.data_ptr(), B, T,
-                                vocab, temperature, top_p, _ptr(uniforms), out_tokens.data_ptr(),
-                                out_accepted.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                _stream_of(dev, stream))
+    return _call_on(dev.index, mk_verify_sample, logits.data_ptr(), _ptr(draft_logits) if T > 1 else None,
+                    tokens.data_ptr(), B, T, vocab, temperature, top_p, _ptr(uniforms), out_tokens.data_ptr(),
+                    out_accepted.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index, stream))
 
 
 def hbm_read_probe(buf, form: int = 0, reps: int = 5, stream=None) -> float:
