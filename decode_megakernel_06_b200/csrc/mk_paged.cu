@@ -1285,7 +1285,7 @@ static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStr
   p.count = static_cast<uint32_t *>(workspace);
   p.part = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + kCountBytes);
   p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD / 4);
-  if (S::kSmem > 46 * 1024) {
+  if (S::kSmem > 40 * 1024) {
     static std::atomic<uint64_t> done{0};  // devices on which the size is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

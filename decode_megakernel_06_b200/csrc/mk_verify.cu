@@ -16,7 +16,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <utility>
+#include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "mk_internal.h"
 
@@ -27,12 +29,17 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 1024;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr double kMassScale = 70368744177664.0;  // 2^46
 constexpr int kBins = 1024;   // histogram bins over max - l
-constexpr int kCand = 512;    // candidates of the threshold bin that one list holds
+constexpr int kFine = 10;     // each of 2^kFine fine ones: 2^20 in all, exact in fp32
+constexpr int kList = 8192;   // logits of the nucleus that a CTA keeps at hand
+constexpr int kCand = 512;    // tokens of the threshold's fine bin that the list holds
+constexpr int kVerifyDevices = 64;
+constexpr int kDrawThreads = 512;
+constexpr int kDrawWarps = kDrawThreads / 32;
 
 // What verify_rows leaves for a row.
 struct RowStat {
@@ -41,7 +48,7 @@ struct RowStat {
   u64 ties;      // tokens tied at tau that belong to the nucleus, lowest ids first
   uint32_t max_key, tau;
   int32_t best;  // argmax (lowest id), temperature <= 0 only
-  int32_t pad;
+  int32_t cut;   // not all tokens at tau belong to the nucleus
 };
 static_assert(sizeof(RowStat) == 40, "workspace layout");
 
@@ -86,69 +93,109 @@ __device__ __forceinline__ u64 nucleus_need(float top_p, u64 total) {
   return need > 0 ? need : 1;
 }
 
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct RowsArgs {
   const float *logits, *draft;
   const int32_t *tokens;
   int B, T, V, slice, vec4, greedy;
   double inv_t;
-  float top_p, bin_scale;
+  float top_p, bin_scale, inv_t2;  // fine bins per unit of the logits; log2(e) / temperature
   RowStat *stats;  // [B * T] target rows, then [B * (T - 1)] draft rows
 };
 
 struct RowsShared {
-  u64 hist[kBins];
-  u64 red[kVWarps], red2[kVWarps];
+  uint32_t hist[kBins];       // read by the cluster
+  u64 fine[1 << kFine];       // read by the cluster
+  u64 red[kVWarps];
+  float wmax[kVWarps], wsum[kVWarps];
   uint32_t wkey[kVWarps];
-  int32_t wid[kVWarps];
-  u64 cta_sum, cta_min;   // read by the cluster
-  u64 least;
-  uint32_t cta_key, n_cand, n_eq;
+  u64 cta_sum, cta_sum2, cta_least;  // read by the cluster
+  float cta_max, cta_weight;
+  uint32_t cta_lo, cta_hi, n_cand;
   int32_t cta_id;
-  uint32_t gmax;
-  u64 total, above, need;
-  int bin;
-  uint32_t cand_key[kCand];
-  u64 cand_mass[kCand];
-  uint32_t tau;
-  u64 tau_above;
+  u64 before, at_tau, same;
+  uint32_t tau, found, n_list;
+  int bin, last_bin;
+  uint32_t cand_key[kCand], all_key[kCand];
+  u64 cand_mass[kCand], all_mass[kCand];
 };
 
-// Sums v over the block; every thread gets the result.
+// The block's sum of v, in every thread.
 __device__ __forceinline__ u64 block_sum(u64 v, u64 *red, int lane, int warp) {
   v = warp_sum(v);
+  __syncthreads();
   if (lane == 0) red[warp] = v;
   __syncthreads();
   u64 s = 0;
 #pragma unroll
   for (int w = 0; w < kVWarps; ++w) s += red[w];
-  __syncthreads();
   return s;
 }
 
-// f(l, id) for this thread's logits of a slice [0, n) of row src (ids from lo).
-template <typename F>
+// The cluster's sum of a value that each CTA holds at *mine (written by thread 0 before
+// the last cluster barrier), in every thread.
+__device__ __forceinline__ u64 cluster_total(cg::cluster_group &cluster, u64 *mine, unsigned size, int lane) {
+  u64 v = lane < (int)size ? *cluster.map_shared_rank(mine, lane) : 0;
+  return warp_sum(v);
+}
+
+// f(l, i) for this thread's logits of the slice [0, n) of a row; padded: the same number
+// of calls in every lane of a warp, with i >= n behind the end.
+template <int UNROLL, typename F>
 __device__ __forceinline__ void each(const float *src, int n, int vec4, int tid, F f) {
   if (vec4) {
     const float4 *s4 = reinterpret_cast<const float4 *>(src);
-#pragma unroll 2
-    for (int i = tid; i < n / 4; i += kVThreads) {
-      const float4 x = s4[i];
-      f(x.x, 4 * i);
-      f(x.y, 4 * i + 1);
-      f(x.z, 4 * i + 2);
-      f(x.w, 4 * i + 3);
+#pragma unroll 1
+    for (int i0 = tid & ~31; i0 < n / 4; i0 += UNROLL * kVThreads) {
+      float4 x[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int i = i0 + (tid & 31) + u * kVThreads;
+        x[u] = i < n / 4 ? s4[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int i = i0 + (tid & 31) + u * kVThreads, at = i < n / 4 ? 4 * i : n;
+        f(x[u].x, at);
+        f(x[u].y, at + 1);
+        f(x[u].z, at + 2);
+        f(x[u].w, at + 3);
+      }
     }
   } else {
-#pragma unroll 4
-    for (int i = tid; i < n; i += kVThreads) f(src[i], i);
+#pragma unroll 1
+    for (int i0 = tid & ~31; i0 < n; i0 += 4 * UNROLL * kVThreads) {
+      float x[4 * UNROLL];
+#pragma unroll
+      for (int u = 0; u < 4 * UNROLL; ++u) {
+        const int i = i0 + (tid & 31) + u * kVThreads;
+        x[u] = i < n ? src[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int u = 0; u < 4 * UNROLL; ++u) f(x[u], min(i0 + (tid & 31) + u * kVThreads, n));
+    }
   }
 }
 
-// One cluster per row.  The row is read from memory once (the largest logit) and
-// then from L2: for the masses' sum, for the histogram, and for the threshold.
-__global__ void __launch_bounds__(kVThreads) verify_rows(const __grid_constant__ RowsArgs a) {
+// One cluster per row (of one CTA where there are rows enough).  The row is read from
+// memory once and from L2 after that: for the largest logit (and an fp32 estimate of
+// the masses' sum), for the masses, and where a nucleus has to be found for its
+// tokens.  The masses, an fp64 exponential per logit, bound this kernel.
+//
+// The nucleus: a token is left out if all tokens whose masses are no larger weigh no
+// more than Q - need, so one whose mass is below (Q - need) / V need not be counted.
+// The others go into a histogram over max - l, bins of equal width, in 32 bits with
+// the row's sum scaled to about 2^30: a guess of the threshold's bin, which the exact
+// sums of the next pass confirm or move.  That bin's tokens go into 1024 finer bins,
+// exactly, whose one holds the threshold: nearly always a single logit, perhaps of
+// many tokens; other keys in it are ranked.
+__global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constant__ RowsArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ RowsShared sh;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  RowsShared &sh = *reinterpret_cast<RowsShared *>(dyn);
+  float *list = reinterpret_cast<float *>(dyn + sizeof(RowsShared));  // [kList]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = cluster.block_rank(), size = cluster.num_blocks();
   const int row = blockIdx.x / size;
@@ -158,248 +205,373 @@ __global__ void __launch_bounds__(kVThreads) verify_rows(const __grid_constant__
   const int lo = (int)rank * a.slice, n = max(0, min(a.slice, a.V - lo));
   const float *base = (is_draft ? a.draft : a.logits) + (size_t)r * a.V;
   const float *src = base + lo;
+  const bool whole = a.top_p >= 1.0f;  // a nucleus is then hardly ever looked for
+  pdl_wait();
+  pdl_launch();
 
-  // ---- the largest logit ---------------------------------------------------------
-  uint32_t kmax = 0;
-  each(src, n, a.vec4, tid, [&](float x, int) { kmax = max(kmax, logit_key(x)); });
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
-  if (lane == 0) sh.wkey[warp] = kmax;
-  for (int i = tid; i < kBins; i += kVThreads) sh.hist[i] = 0;
-  if (tid == 0) sh.n_cand = 0;
+  // ---- the largest logit; for a nucleus also about how much the masses weigh --------------
+  float mx = -INFINITY, wt = 0.f;
+  if (whole || a.greedy) {
+    each<4>(src, n, a.vec4, tid, [&](float x, int) { mx = fmaxf(mx, x); });
+  } else {
+    each<2>(src, n, a.vec4, tid, [&](float x, int) {
+      if (x > mx) {
+        wt *= exp2f((mx - x) * a.inv_t2);
+        mx = x;
+      }
+      wt += mx > -INFINITY ? exp2f((x - mx) * a.inv_t2) : 0.f;
+    });
+  }
+  auto fold = [&](int width) {  // (mx, wt) over groups of `width` lanes
+    for (int o = width / 2; o; o >>= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, mx, o), ow = __shfl_xor_sync(0xffffffffu, wt, o);
+      const float to = fmaxf(mx, om);
+      wt = to == -INFINITY ? 0.f : wt * exp2f((mx - to) * a.inv_t2) + ow * exp2f((om - to) * a.inv_t2);
+      mx = to;
+    }
+  };
+  fold(32);
+  if (lane == 0) {
+    sh.wmax[warp] = mx;
+    sh.wsum[warp] = wt;
+  }
+  if (!whole)
+    for (int i = tid; i < kBins; i += kVThreads) sh.hist[i] = 0;
+  if (tid == 0) sh.n_list = sh.n_cand = 0;
   __syncthreads();
-  if (tid == 0) {
-    uint32_t k = 0;
-    for (int w = 0; w < kVWarps; ++w) k = max(k, sh.wkey[w]);
-    sh.cta_key = k;
+  if (warp == 0) {
+    mx = sh.wmax[lane];
+    wt = sh.wsum[lane];
+    fold(32);
+    if (lane == 0) {
+      sh.cta_max = mx;
+      sh.cta_weight = wt;
+    }
   }
   cluster.sync();
-  if (tid == 0) {
-    uint32_t k = 0;
-    for (unsigned i = 0; i < size; ++i) k = max(k, *cluster.map_shared_rank(&sh.cta_key, i));
-    sh.gmax = k;
-  }
-  __syncthreads();
-  const uint32_t gmax = sh.gmax;
+  mx = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_max, lane) : -INFINITY;
+  wt = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_weight, lane) : 0.f;
+  fold(32);
+  const float m = mx;
+  const uint32_t gmax = logit_key(m);
 
   if (a.greedy) {
     int best = 0x7fffffff;
-    each(src, n, a.vec4, tid, [&](float x, int i) {
-      if (logit_key(x) == gmax) best = min(best, lo + i);
+    each<4>(src, n, a.vec4, tid, [&](float x, int i) {
+      if (x == m && i < n) best = min(best, lo + i);
     });
     best = __reduce_min_sync(0xffffffffu, best);
-    if (lane == 0) sh.wid[warp] = best;
+    if (lane == 0) sh.wkey[warp] = best;
     __syncthreads();
-    if (tid == 0) {
-      int m = 0x7fffffff;
-      for (int w = 0; w < kVWarps; ++w) m = min(m, sh.wid[w]);
-      sh.cta_id = m;
+    if (warp == 0) {
+      const int v = __reduce_min_sync(0xffffffffu, static_cast<int>(sh.wkey[lane]));
+      if (lane == 0) sh.cta_id = v;
     }
     cluster.sync();
-    if (rank == 0 && tid == 0) {
-      int m = 0x7fffffff;
-      for (unsigned i = 0; i < size; ++i) m = min(m, *cluster.map_shared_rank(&sh.cta_id, i));
-      a.stats[row].best = m;
+    if (rank == 0 && warp == 0) {
+      const int v = __reduce_min_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_id, lane) : 0x7fffffff);
+      if (lane == 0) a.stats[row].best = min(v, a.V - 1);
     }
     cluster.sync();  // no CTA leaves while its shared memory is being read
     return;
   }
 
-  // ---- the masses' sum and the smallest that is not zero -----------------------------
-  const float m = key_logit(gmax);
-  const bool whole = a.top_p >= 1.0f;  // the histogram is then hardly ever needed
+  auto fine_of = [&](float v) {
+    return max((int)fminf((m - v) * a.bin_scale, (float)((kBins << kFine) - 1)), 0);
+  };
+  // ---- the masses' sum and the smallest that is not zero; the guess' histogram ---------------
   u64 sum = 0, least = ~0ull;
-  each(src, n, a.vec4, tid, [&](float x, int) {
-    const u64 q = mass_of(x, m, a.inv_t);
-    if (q) {
+  {
+    // weights are relative to the largest mass 2^46; wt < 2 kMaxVocab
+    const float up = 1073741824.0f / fmaxf(wt, 1.f);  // mass 2^46 in the histogram's unit
+    const double scale = (double)up / kMassScale;
+    const u64 skip = (u64)(0.99 * fmin(1.0, fmax(0.0, 1.0 - (double)a.top_p)) * (double)wt * kMassScale / a.V);
+    each<1>(src, n, a.vec4, tid, [&](float x, int) {
+      const u64 q = mass_of(x, m, a.inv_t);
       sum += q;
-      least = min(least, q);
-      if (!whole) {
-        const int bin = (int)fminf((m - x) * a.bin_scale, (float)(kBins - 1));
-        atomicAdd(&sh.hist[max(bin, 0)], q);
-      }
-    }
-  });
+      if (q) least = min(least, q);
+      if (!whole && q > skip) atomicAdd(&sh.hist[fine_of(x) >> kFine], __double2uint_rn(__ull2double_rn(q) * scale));
+    });
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-  if (lane == 0) sh.red2[warp] = least;
   sum = block_sum(sum, sh.red, lane, warp);
-  if (tid == 0) {
-    u64 x = ~0ull;
-    for (int w = 0; w < kVWarps; ++w) x = min(x, sh.red2[w]);
-    sh.cta_sum = sum;
-    sh.cta_min = x;
+  __syncthreads();
+  if (lane == 0) sh.red[warp] = least;
+  __syncthreads();
+  if (warp == 0) {
+    u64 v = sh.red[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (lane == 0) {
+      sh.cta_sum = sum;
+      sh.cta_least = v;
+    }
   }
   cluster.sync();
-  if (tid == 0) {
-    u64 s = 0, x = ~0ull;
-    for (unsigned i = 0; i < size; ++i) {
-      s += *cluster.map_shared_rank(&sh.cta_sum, i);
-      x = min(x, *cluster.map_shared_rank(&sh.cta_min, i));
-    }
-    sh.total = s;
-    sh.least = x;
-    sh.need = nucleus_need(a.top_p, s);
-  }
-  __syncthreads();
-  const u64 total = sh.total, need = sh.need;
-  cluster.sync();  // cta_sum is written again
-  const u64 smallest = sh.least;
+  const u64 total = cluster_total(cluster, &sh.cta_sum, size, lane);
+  u64 smallest = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_least, lane) : ~0ull;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) smallest = min(smallest, __shfl_xor_sync(0xffffffffu, smallest, o));
+  const u64 need = nucleus_need(a.top_p, total);
 
   uint32_t tau = 0;       // every token with a mass
-  u64 ties = 0, mass = total;
+  u64 ties = 0, nucleus = total;
+  bool cut = false;
   if (smallest <= total - need) {  // some token may be left out
-    // ---- the bin that holds the threshold ---------------------------------------------
-    if (whole) {
-      each(src, n, a.vec4, tid, [&](float x, int) {
-        const u64 q = mass_of(x, m, a.inv_t);
-        if (q) {
-          const int bin = (int)fminf((m - x) * a.bin_scale, (float)(kBins - 1));
-          atomicAdd(&sh.hist[max(bin, 0)], q);
-        }
-      });
-    }
-    __syncthreads();
-    cluster.sync();
-    u64 v[kBins / kVThreads], s = 0;
+    // ---- the guess: the bin where the scaled sums reach need ------------------------------
+    // for top_p = 1 (fp64 rounded need below Q) at most 2^10 units are left out: the last bin with
+    // a mass, or one shortly before it
+    int bin = min(kBins - 1, (int)((31.9 - log(__ull2double_rn(smallest))) * (kBins / 33.0)) + 1);
+    if (!whole) {
+      const uint32_t v = [&] {
+        uint32_t x = 0;
+        for (unsigned i = 0; i < size; ++i) x += cluster.map_shared_rank(&sh.hist[0], i)[tid];
+        return x;
+      }();
+      static_assert(kBins == kVThreads && (1 << kFine) == kVThreads, "a thread per bin");
+      uint32_t incl = v;
 #pragma unroll
-    for (int k = 0; k < kBins / kVThreads; ++k) {
-      v[k] = 0;
-      for (unsigned i = 0; i < size; ++i)
-        v[k] += *cluster.map_shared_rank(&sh.hist[tid * (kBins / kVThreads) + k], i);
-      s += v[k];
-    }
-    u64 incl = warp_scan(s, lane);
-    if (lane == 31) sh.red[warp] = incl;
-    if (tid == 0) {  // reached only if no bin is found (non-finite logits)
-      sh.bin = kBins - 1;
-      sh.above = 0;
-    }
-    __syncthreads();
-    u64 before = incl - s;
-    for (int w = 0; w < warp; ++w) before += sh.red[w];
-#pragma unroll
-    for (int k = 0; k < kBins / kVThreads; ++k) {
-      if (before < need && before + v[k] >= need) {
-        sh.bin = tid * (kBins / kVThreads) + k;
-        sh.above = before;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t w = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += w;
       }
-      before += v[k];
-    }
-    __syncthreads();
-    const int bin = sh.bin;
-    const u64 above = sh.above;
-    // ---- the tokens of that bin --------------------------------------------------------
-    each(src, n, a.vec4, tid, [&](float x, int) {
-      const int i = max((int)fminf((m - x) * a.bin_scale, (float)(kBins - 1)), 0);
-      if (i == bin) {
-        const u64 q = mass_of(x, m, a.inv_t);
-        if (q) {
-          const uint32_t at = atomicAdd(&sh.n_cand, 1u);
-          if (at < kCand) {
-            sh.cand_key[at] = logit_key(x);
-            sh.cand_mass[at] = q;
-          }
-        }
-      }
-    });
-    if (tid == 0) {  // before the barrier: another CTA may write them after it
-      sh.tau = 0;
-      sh.tau_above = above;
-    }
-    cluster.sync();
-    // Every CTA decides from the same lists.  tau is the key of the candidate with
-    // mass(bins above) + mass(candidates above it) < need <= that + its ties' mass.
-    bool fits = true;
-    for (unsigned i = 0; i < size; ++i) fits = fits && *cluster.map_shared_rank(&sh.n_cand, i) <= kCand;
-    if (fits) {
-      const uint32_t own = sh.n_cand;
-      for (uint32_t c = tid; c < own; c += kVThreads) {
-        const uint32_t key = sh.cand_key[c];
-        u64 more = above, same = 0;
-        for (unsigned i = 0; i < size; ++i) {
-          const uint32_t cnt = *cluster.map_shared_rank(&sh.n_cand, i);
-          const uint32_t *ck = cluster.map_shared_rank(sh.cand_key, i);
-          const u64 *cm = cluster.map_shared_rank(sh.cand_mass, i);
-          for (uint32_t j = 0; j < cnt; ++j) {
-            const uint32_t kj = ck[j];
-            if (kj > key) more += cm[j];
-            else if (kj == key) same += cm[j];
-          }
-        }
-        if (more < need && need <= more + same)  // tied candidates write the same values, in every CTA
-          for (unsigned i = 0; i < size; ++i) {
-            *cluster.map_shared_rank(&sh.tau, i) = key;
-            *cluster.map_shared_rank(&sh.tau_above, i) = more;
-          }
-      }
-      cluster.sync();
-    } else {
-      // Too many for the list (a row of equal logits): bisection of the key, bit
-      // by bit, for the largest key with mass(keys >= it) >= need.
-      uint32_t lo_key = 0;
-      for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t mid = lo_key | (1u << bit);
-        u64 part = 0;
-        each(src, n, a.vec4, tid, [&](float x, int) {
-          if (logit_key(x) >= mid) part += mass_of(x, m, a.inv_t);
-        });
-        part = block_sum(part, sh.red, lane, warp);
-        if (tid == 0) sh.cta_sum = part;
-        cluster.sync();
-        u64 all = 0;
-        for (unsigned i = 0; i < size; ++i) all += *cluster.map_shared_rank(&sh.cta_sum, i);
-        cluster.sync();
-        if (all >= need) lo_key = mid;
-      }
-      u64 part = 0;
-      each(src, n, a.vec4, tid, [&](float x, int) {
-        if (logit_key(x) > lo_key) part += mass_of(x, m, a.inv_t);
-      });
-      part = block_sum(part, sh.red, lane, warp);
-      if (tid == 0) sh.cta_sum = part;
-      cluster.sync();
-      u64 all = 0;
-      for (unsigned i = 0; i < size; ++i) all += *cluster.map_shared_rank(&sh.cta_sum, i);
-      cluster.sync();
+      if (lane == 31) sh.wkey[warp] = incl;
       if (tid == 0) {
-        sh.tau = lo_key;
-        sh.tau_above = all;
+        sh.bin = kBins;
+        sh.last_bin = 0;
       }
       __syncthreads();
+      uint32_t w = sh.wkey[lane];
+      w = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
+      incl += w;
+      const double want = __ull2double_rn(need) * (1073741824.0 / fmaxf(wt, 1.f)) / kMassScale;
+      if (v && (double)incl >= want) atomicMin(&sh.bin, tid);
+      if (v) atomicMax(&sh.last_bin, tid);
+      __syncthreads();
+      bin = min(sh.bin, sh.last_bin);
     }
-    tau = sh.tau;
-    const u64 at_tau = sh.tau_above;
+    // ---- the exact sum above the bin and in it; the bin moves where the guess was off ---------
+    u64 above = 0;
+    bool listed = false;
+#pragma unroll 1
+    for (int tries = 0; tries < kBins; ++tries) {
+      each<2>(src, n, a.vec4, tid, [&](float x, int i) {
+        const bool in = i < n && (fine_of(x) >> kFine) <= bin;
+        const unsigned hit = __ballot_sync(0xffffffffu, in);
+        uint32_t at = 0;
+        if (hit && lane == 0) at = atomicAdd(&sh.n_list, (uint32_t)__popc(hit));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1u));
+        if (in && at < kList) list[at] = x;
+      });
+      __syncthreads();
+      listed = sh.n_list <= kList;
+      u64 more = 0, in = 0;
+      auto add = [&](float x, int i) {
+        const int at = fine_of(x) >> kFine;
+        if (i >= n || at > bin) return;
+        const u64 q = mass_of(x, m, a.inv_t);
+        if (at < bin) more += q;
+        else in += q;
+      };
+      if (listed) {
+#pragma unroll 1
+        for (uint32_t k = tid; k < sh.n_list; k += kVThreads) add(list[k], 0);
+      } else {
+        each<1>(src, n, a.vec4, tid, add);
+      }
+      more = block_sum(more, sh.red, lane, warp);
+      in = block_sum(in, sh.red, lane, warp);
+      if (tid == 0) {
+        sh.cta_sum = more;
+        sh.cta_sum2 = in;
+      }
+      cluster.sync();
+      above = cluster_total(cluster, &sh.cta_sum, size, lane);
+      const u64 inside = cluster_total(cluster, &sh.cta_sum2, size, lane);
+      const bool up = above >= need && bin > 0, down = above + inside < need && bin < kBins - 1;
+      if (!up && !down) break;
+      bin += up ? -1 : 1;
+      cluster.sync();  // the sums have been read
+      if (tid == 0) sh.n_list = 0;
+      __syncthreads();
+    }
+    // f(l) for the bin's tokens in this CTA
+    auto of_bin = [&](auto f) {
+      if (listed) {
+#pragma unroll 1
+        for (uint32_t k = tid; k < sh.n_list; k += kVThreads)
+          if ((fine_of(list[k]) >> kFine) == bin) f(list[k]);
+      } else {
+        each<1>(src, n, a.vec4, tid, [&](float x, int i) {
+          if (i < n && (fine_of(x) >> kFine) == bin) f(x);
+        });
+      }
+    };
+    // ---- its fine bins, exactly -----------------------------------------------------------
+    sh.fine[tid] = 0;
+    __syncthreads();
+    of_bin([&](float x) {
+      const u64 q = mass_of(x, m, a.inv_t);
+      if (q) atomicAdd(&sh.fine[fine_of(x) & ((1 << kFine) - 1)], q);
+    });
+    cluster.sync();
+    u64 v = 0;
+    for (unsigned i = 0; i < size; ++i) v += cluster.map_shared_rank(&sh.fine[0], i)[tid];
+    u64 incl = warp_scan(v, lane);
+    if (lane == 31) sh.red[warp] = incl;
+    if (tid == 0) {  // kept only on non-finite input
+      sh.bin = 0;
+      sh.before = above;
+      sh.found = 0;
+      sh.n_cand = 0;
+    }
+    __syncthreads();
+    incl += above + warp_sum(lane < warp ? sh.red[lane] : 0);
+    if (incl - v < need && need <= incl) {
+      sh.bin = tid;
+      sh.before = incl - v;
+    }
+    __syncthreads();
+    const int fine = sh.bin | bin << kFine;
+    const u64 before = sh.before;
+    u64 at_tau = before, same = 0;
+    // ---- its tokens: one key, or a list of them to rank ------------------------------------------
+    uint32_t klo = 0xffffffffu, khi = 0;
+    of_bin([&](float x) {
+      if (fine_of(x) != fine) return;
+      const uint32_t key = logit_key(x);
+      klo = min(klo, key);
+      khi = max(khi, key);
+      const uint32_t at = atomicAdd(&sh.n_cand, 1u);
+      if (at < kCand) {
+        sh.cand_key[at] = key;
+        sh.cand_mass[at] = mass_of(x, m, a.inv_t);
+      }
+    });
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    if (lane == 0) sh.wkey[warp] = klo;
+    __syncthreads();
+    if (warp == 0) {
+      klo = __reduce_min_sync(0xffffffffu, sh.wkey[lane]);
+      if (lane == 0) sh.cta_lo = klo;
+    }
+    __syncthreads();
+    if (lane == 0) sh.wkey[warp] = khi;
+    __syncthreads();
+    if (warp == 0) {
+      khi = __reduce_max_sync(0xffffffffu, sh.wkey[lane]);
+      if (lane == 0) sh.cta_hi = khi;
+    }
+    cluster.sync();
+    klo = __reduce_min_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_lo, lane) : 0xffffffffu);
+    khi = __reduce_max_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_hi, lane) : 0u);
+    const uint32_t cnt = lane < (int)size ? *cluster.map_shared_rank(&sh.n_cand, lane) : 0u;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, cnt);
+    if (klo == khi) {
+      tau = klo;
+      same = cluster_total(cluster, &sh.fine[fine & ((1 << kFine) - 1)], size, lane);
+    } else if (all <= kCand) {
+      uint32_t first = cnt;
+#pragma unroll
+      for (int o = 1; o < kMaxCluster; o <<= 1) {
+        const uint32_t w = __shfl_up_sync(0xffffffffu, first, o);
+        if (lane >= o) first += w;
+      }
+      first -= cnt;  // entries of the CTAs before CTA `lane`
+      for (unsigned i = 0; i < size; ++i) {
+        const uint32_t f = __shfl_sync(0xffffffffu, first, i), c = __shfl_sync(0xffffffffu, cnt, i);
+        const uint32_t *ck = cluster.map_shared_rank(sh.cand_key, i);
+        const u64 *cm = cluster.map_shared_rank(sh.cand_mass, i);
+        for (uint32_t k = tid; k < c; k += kVThreads) {
+          sh.all_key[f + k] = ck[k];
+          sh.all_mass[f + k] = cm[k];
+        }
+      }
+      __syncthreads();
+      // tau is the key with sum(above it) < need <= sum(above it) + its ties' sum
+      if (tid < (int)all) {
+        const uint32_t key = sh.all_key[tid];
+        u64 over = before, tied = 0;
+#pragma unroll 4
+        for (uint32_t e = 0; e < all; ++e) {
+          const uint32_t ke = sh.all_key[e];
+          const u64 qe = sh.all_mass[e];
+          if (ke > key) over += qe;
+          if (ke == key) tied += qe;
+        }
+        if (over < need && need <= over + tied) {  // tied tokens write the same values
+          sh.tau = key;
+          sh.at_tau = over;
+          sh.same = tied;
+          sh.found = 1;
+        }
+      }
+      __syncthreads();
+      if (sh.found) {
+        tau = sh.tau;
+        at_tau = sh.at_tau;
+        same = sh.same;
+      }
+    } else {
+      // More than the list holds, and not one key: the keys between klo and khi are halved
+      // until one is left, the largest with sum(keys >= it) >= need.
+      auto sum_from = [&](uint32_t key, bool only) {
+        u64 part = 0;
+        of_bin([&](float x) {
+          const uint32_t k = logit_key(x);
+          if (fine_of(x) == fine && (only ? k == key : k >= key)) part += mass_of(x, m, a.inv_t);
+        });
+        part = block_sum(part, sh.red, lane, warp);
+        cluster.sync();  // cta_sum has been read
+        if (tid == 0) sh.cta_sum = part;
+        cluster.sync();
+        return cluster_total(cluster, &sh.cta_sum, size, lane);
+      };
+      while (klo < khi) {
+        const uint32_t mid = klo + (khi - klo + 1) / 2;
+        if (before + sum_from(mid, false) >= need) klo = mid;
+        else khi = mid - 1;
+      }
+      tau = klo;
+      at_tau = before + sum_from(tau, false);
+      same = sum_from(tau, true);
+      at_tau -= same;
+    }
+    cluster.sync();  // cta_sum is written again below
     u64 q_tau = mass_of(key_logit(tau), m, a.inv_t);
     if (q_tau == 0) q_tau = 1;  // only on non-finite input
     ties = need > at_tau ? (need - at_tau + q_tau - 1) / q_tau : 1;
-    mass = at_tau + ties * q_tau;
+    nucleus = at_tau + ties * q_tau;
+    cut = ties * q_tau < same;
   }
 
   // ---- the draft that this row decides on ---------------------------------------------
-  const int x = t < a.T - 1 ? a.tokens[b * a.T + t + 1] : -1;
+  const int d = t < a.T - 1 ? a.tokens[b * a.T + t + 1] : -1;
   u64 drafted = 0;
-  if (x >= 0 && x < a.V) {
-    const uint32_t key = logit_key(base[x]);
-    if (key > tau) {
-      drafted = mass_of(base[x], m, a.inv_t);
+  if (d >= 0 && d < a.V) {
+    const float l = base[d];
+    const uint32_t key = logit_key(l);
+    if (key > tau || (key == tau && !cut)) {
+      drafted = mass_of(l, m, a.inv_t);
     } else if (key == tau) {  // in the nucleus if fewer than `ties` of its ties have lower ids
       u64 lower = 0;
-      each(src, n, a.vec4, tid, [&](float y, int i) { lower += logit_key(y) == tau && lo + i < x; });
+      each<2>(src, n, a.vec4, tid, [&](float y, int i) { lower += logit_key(y) == tau && i < n && lo + i < d; });
       lower = block_sum(lower, sh.red, lane, warp);
       if (tid == 0) sh.cta_sum = lower;
       cluster.sync();
-      u64 all = 0;
-      for (unsigned i = 0; i < size; ++i) all += *cluster.map_shared_rank(&sh.cta_sum, i);
-      if (all < ties) drafted = mass_of(base[x], m, a.inv_t);
+      if (cluster_total(cluster, &sh.cta_sum, size, lane) < ties) drafted = mass_of(l, m, a.inv_t);
     }
   }
   if (rank == 0 && tid == 0) {
     RowStat &o = a.stats[row];
-    o.mass = mass;
+    o.mass = nucleus;
     o.drafted = drafted;
     o.ties = ties;
     o.max_key = gmax;
     o.tau = tau;
+    o.cut = cut;
   }
   cluster.sync();  // no CTA leaves while its shared memory is being read
 }
@@ -408,179 +580,202 @@ struct DrawArgs {
   const float *logits, *draft;
   const int32_t *tokens;
   const double *uniforms;
-  int B, T, V, slice, greedy;
+  int B, T, V, slice, per, greedy;  // ids per CTA and per warp (a multiple of 32)
   double inv_t;
   const RowStat *stats;
   int32_t *out_tokens, *out_accepted;
 };
 
-// One row's membership: mass of id with logit l, `tied` of its ties before it.
+// A row's nucleus: the mass of an id with logit l, `tied` of its ties before it.
 struct RowMass {
   float m;
   uint32_t tau;
   u64 ties;
   double inv_t;
-  __device__ u64 of(float l, uint32_t key, u64 tied) const {
-    if (key > tau || (key == tau && tied < ties)) return mass_of(l, m, inv_t);
-    return 0;
+  bool cut;
+  __device__ __forceinline__ u64 of(float l, u64 tied) const {
+    const uint32_t key = logit_key(l);
+    return key > tau || (key == tau && (!cut || tied < ties)) ? mass_of(l, m, inv_t) : 0;
   }
 };
 
-// One cluster per sequence; warp w of CTA r holds segment r * kVWarps + w of the
-// row's ids.  Ties at the two thresholds are counted per segment first, so that
-// a token's rank among its ties is known when its mass is taken.
-__global__ void __launch_bounds__(kVThreads) verify_draw(const __grid_constant__ DrawArgs a) {
+// One cluster per sequence; warp w of CTA r holds ids r * slice + w * per, .. in id
+// order, and keeps the masses that they are drawn with in shared memory: the sums
+// of the segments give the one that holds the draw's point, and its warp scans it.
+// Where a threshold cuts through tied tokens, their ranks are counted first.
+__global__ void __launch_bounds__(kDrawThreads) verify_draw(const __grid_constant__ DrawArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ u64 red[kVWarps], seg[kVWarps];
-  __shared__ uint32_t tie_a[kVWarps], tie_d[kVWarps];
+  extern __shared__ u64 mass[];  // [kDrawWarps][per]
+  __shared__ u64 seg[kDrawWarps];
+  __shared__ uint32_t tie_a[kDrawWarps], tie_d[kDrawWarps];
   __shared__ u64 c_sum;
-  __shared__ uint32_t c_tie[2];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ u64 c_tie[2];
+  pdl_wait();
+  pdl_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = cluster.block_rank(), size = cluster.num_blocks();
   const int b = blockIdx.x / size, T = a.T;
   const RowStat *st = a.stats + (size_t)b * T;
   const RowStat *sd = a.stats + (size_t)a.B * T + (size_t)b * (T - 1);
   const int32_t *tok = a.tokens + (size_t)b * T;
+  int32_t *out = a.out_tokens + (size_t)b * T;
   const bool lead = rank == 0 && tid == 0;
 
-  // ---- how many drafts stand ------------------------------------------------------
+  // ---- how many drafts stand: a lane each ---------------------------------------------
   int s = 0;
-  for (; s < T - 1; ++s) {
-    const int x = tok[s + 1];
-    if (x < 0 || x >= a.V) break;
-    if (a.greedy) {
-      if (x != st[s].best) break;
-      continue;
+  for (int s0 = 0; s0 < T; s0 += 32) {
+    const int i = s0 + lane;
+    bool ok = false;
+    const int x = i < T - 1 ? tok[i + 1] : -1;
+    if (x >= 0 && x < a.V) {
+      if (a.greedy) {
+        ok = x == st[i].best;
+      } else {
+        const double u = a.uniforms[(size_t)b * T + i];
+        const double am = __ull2double_rn(st[i].mass), ax = __ull2double_rn(st[i].drafted);
+        if (a.draft) {
+          const double dm = __ull2double_rn(sd[i].mass), dx = __ull2double_rn(sd[i].drafted);
+          ok = __dmul_rn(u, __dmul_rn(dx, am)) < __dmul_rn(ax, dm);
+        } else {
+          ok = __dmul_rn(u, am) < ax;
+        }
+      }
     }
-    double u = a.uniforms[(size_t)b * T + s];
-    const double am = __ull2double_rn(st[s].mass), ax = __ull2double_rn(st[s].drafted);
-    bool ok;
-    if (a.draft) {
-      const double dm = __ull2double_rn(sd[s].mass), dx = __ull2double_rn(sd[s].drafted);
-      ok = __dmul_rn(u, __dmul_rn(dx, am)) < __dmul_rn(ax, dm);
-    } else {
-      ok = __dmul_rn(u, am) < ax;
+    const unsigned bad = ~__ballot_sync(0xffffffffu, ok);
+    if (bad) {  // lane T - 1 at the latest
+      s = s0 + __ffs(bad) - 1;
+      break;
     }
-    if (!ok) break;
   }
-  if (lead) {
-    a.out_accepted[b] = s + 1;
-    for (int i = 0; i < T; ++i)
-      if (i != s) a.out_tokens[(size_t)b * T + i] = i < s ? tok[i + 1] : -1;
+  if (rank == 0) {
+    for (int i = tid; i < T; i += kDrawThreads)
+      if (i != s) out[i] = i < s ? tok[i + 1] : -1;
+    if (tid == 0) a.out_accepted[b] = s + 1;
   }
   if (a.greedy) {
-    if (lead) a.out_tokens[(size_t)b * T + s] = st[s].best;
+    if (lead) out[s] = st[s].best;
     return;
   }
 
   const int x = s < T - 1 ? tok[s + 1] : -1;
-  bool residual = x >= 0 && x < a.V;  // a draft that did not stand
-  const float *la = a.logits + ((size_t)b * T + s) * a.V;
+  const bool residual = x >= 0 && x < a.V;  // a draft that did not stand
   const bool with_d = residual && a.draft;
-  const float *ld = with_d ? a.draft + ((size_t)b * (T - 1) + s) * a.V : nullptr;
-  const RowMass A{key_logit(st[s].max_key), st[s].tau, st[s].ties, a.inv_t};
-  const RowMass D = with_d ? RowMass{key_logit(sd[s].max_key), sd[s].tau, sd[s].ties, a.inv_t} : A;
+  const float *la = a.logits + ((size_t)b * T + s) * a.V;
+  const float *ld = with_d ? a.draft + ((size_t)b * (T - 1) + s) * a.V : la;
+  const RowMass A{key_logit(st[s].max_key), st[s].tau, st[s].ties, a.inv_t, st[s].cut != 0};
+  const RowMass D = with_d ? RowMass{key_logit(sd[s].max_key), sd[s].tau, sd[s].ties, a.inv_t, sd[s].cut != 0} : A;
   const double ra = with_d ? kMassScale / __ull2double_rn(st[s].mass) : 0.0;
   const double rd = with_d ? kMassScale / __ull2double_rn(sd[s].mass) : 0.0;
-
-  const int per = (a.slice + kVWarps - 1) / kVWarps;
   const int lo = (int)rank * a.slice, hi = min(a.V, lo + a.slice);
-  const int s0 = min(hi, lo + warp * per), s1 = min(hi, s0 + per);
+  const int s0 = min(hi, lo + warp * a.per), s1 = min(hi, s0 + a.per);
+  u64 *mine = mass + warp * a.per;
 
-  // ---- ties before each segment ------------------------------------------------------
-  uint32_t ca = 0, cd = 0;
-  for (int i = s0 + lane; i < s1; i += 32) {
-    ca += logit_key(la[i]) == A.tau;
-    if (with_d) cd += logit_key(ld[i]) == D.tau;
-  }
-  ca = __reduce_add_sync(0xffffffffu, ca);
-  cd = __reduce_add_sync(0xffffffffu, cd);
-  if (lane == 0) {
-    tie_a[warp] = ca;
-    tie_d[warp] = cd;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    c_tie[0] = c_tie[1] = 0;
-    for (int w = 0; w < kVWarps; ++w) {
-      c_tie[0] += tie_a[w];
-      c_tie[1] += tie_d[w];
-    }
-  }
-  cluster.sync();
+  // ---- ties before each segment, where they matter ----------------------------------------
+  const bool cut = A.cut || (with_d && D.cut);
   u64 before_a = 0, before_d = 0;
-  for (unsigned i = 0; i < rank; ++i) {
-    const uint32_t *o = cluster.map_shared_rank(c_tie, i);
-    before_a += o[0];
-    before_d += o[1];
-  }
-  for (int w = 0; w < warp; ++w) {
-    before_a += tie_a[w];
-    before_d += tie_d[w];
-  }
-
-  // The mass that id i (this lane's of 32 neighbours) is drawn with; ta, td count
-  // the ties before these 32.
-  auto mass_at = [&](int i, bool in, bool res, u64 &ta, u64 &td) -> u64 {
-    const float l = in ? la[i] : 0.f;
-    const uint32_t k = in ? logit_key(l) : 0u;
-    const unsigned eq = __ballot_sync(0xffffffffu, in && k == A.tau);
-    u64 q = in ? A.of(l, k, ta + __popc(eq & ((1u << lane) - 1u))) : 0;
-    ta += __popc(eq);
-    if (!res) return q;
-    if (!with_d) return i == x ? 0 : q;
-    const float y = in ? ld[i] : 0.f;
-    const uint32_t kd = in ? logit_key(y) : 0u;
-    const unsigned ed = __ballot_sync(0xffffffffu, in && kd == D.tau);
-    const u64 w = in ? D.of(y, kd, td + __popc(ed & ((1u << lane) - 1u))) : 0;
-    td += __popc(ed);
-    const u64 p = __double2ull_rn(__dmul_rn(__ull2double_rn(q), ra)), o = __double2ull_rn(__dmul_rn(__ull2double_rn(w), rd));
-    return p > o ? p - o : 0;
-  };
-
-  // ---- the masses' sums: the residual's, and the target's own where that is zero -------
-  u64 total = 0;
-  for (int round = residual ? 0 : 1; round < 2; ++round) {
-    const bool res = round == 0;
-    u64 ta = before_a, td = before_d, mine = 0;
-    for (int i0 = s0; i0 < s1; i0 += 32) mine += mass_at(i0 + lane, i0 + lane < s1, res, ta, td);
-    mine = warp_sum(mine);
-    if (lane == 0) seg[warp] = mine;
+  if (cut) {
+    uint32_t ca = 0, cd = 0;
+#pragma unroll 4
+    for (int i = s0 + lane; i < s1; i += 32) {
+      ca += logit_key(la[i]) == A.tau;
+      if (with_d) cd += logit_key(ld[i]) == D.tau;
+    }
+    ca = __reduce_add_sync(0xffffffffu, ca);
+    cd = __reduce_add_sync(0xffffffffu, cd);
+    if (lane == 0) {
+      tie_a[warp] = ca;
+      tie_d[warp] = cd;
+    }
     __syncthreads();
     if (tid == 0) {
-      u64 c = 0;
-      for (int w = 0; w < kVWarps; ++w) c += seg[w];
-      c_sum = c;
+      c_tie[0] = c_tie[1] = 0;
+      for (int w = 0; w < kDrawWarps; ++w) {
+        c_tie[0] += tie_a[w];
+        c_tie[1] += tie_d[w];
+      }
     }
     cluster.sync();
-    total = 0;
-    u64 before = 0;
-    for (unsigned i = 0; i < size; ++i) {
-      const u64 c = *cluster.map_shared_rank(&c_sum, i);
-      if (i < rank) before += c;
-      total += c;
+    for (unsigned i = 0; i < rank; ++i) {
+      const u64 *o = cluster.map_shared_rank(c_tie, i);
+      before_a += o[0];
+      before_d += o[1];
     }
-    for (int w = 0; w < warp; ++w) before += seg[w];
-    const u64 own = seg[warp];
+    for (int w = 0; w < warp; ++w) {
+      before_a += tie_a[w];
+      before_d += tie_d[w];
+    }
+  }
+
+  // ---- the masses and their sum: the residual's, and the target's own where that is zero ----
+  for (int round = residual ? 0 : 1; round < 2; ++round) {
+    const bool res = round == 0, two = res && with_d;
+    u64 ta = before_a, td = before_d, sum = 0;
+    constexpr int kBatch = 8;  // loads in flight per lane and row
+#pragma unroll 1
+    for (int i0 = s0; i0 < s1; i0 += 32 * kBatch) {
+      float va[kBatch], vd[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + 32 * k + lane;
+        va[k] = i < s1 ? la[i] : -INFINITY;
+        vd[k] = two && i < s1 ? ld[i] : -INFINITY;
+      }
+#pragma unroll 1
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + 32 * k + lane;
+        if (i0 + 32 * k >= s1) break;
+        const float l = va[k], y = vd[k];
+        u64 na = ta, nd = td;
+        if (cut) {
+          const unsigned ea = __ballot_sync(0xffffffffu, i < s1 && logit_key(l) == A.tau);
+          const unsigned ed = __ballot_sync(0xffffffffu, two && i < s1 && logit_key(y) == D.tau);
+          na += __popc(ea & ((1u << lane) - 1u));
+          nd += __popc(ed & ((1u << lane) - 1u));
+          ta += __popc(ea);
+          td += __popc(ed);
+        }
+        u64 q = i < s1 ? A.of(l, na) : 0;
+        if (two) {
+          const u64 w = i < s1 ? D.of(y, nd) : 0;
+          const u64 p = __double2ull_rn(__dmul_rn(__ull2double_rn(q), ra)), o = __double2ull_rn(__dmul_rn(__ull2double_rn(w), rd));
+          q = p > o ? p - o : 0;
+        } else if (res && i == x) {
+          q = 0;
+        }
+        if (i < s1) mine[i - s0] = q;
+        sum += q;
+      }
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) seg[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const u64 c = warp_sum(lane < kDrawWarps ? seg[lane] : 0);
+      if (lane == 0) c_sum = c;
+    }
+    cluster.sync();
+    const u64 c = lane < (int)size ? *cluster.map_shared_rank(&c_sum, lane) : 0;
+    const u64 total = warp_sum(c);
+    u64 before = warp_sum(lane < (int)rank ? c : 0);
     if (res && total == 0) {
       cluster.sync();  // c_sum and seg are written again
       continue;
     }
+    before += warp_sum(lane < warp ? seg[lane] : 0);
     // ---- the draw: the segment that holds y, then the id in it -------------------------
     double uu = a.uniforms[(size_t)b * T + T - 1];
     if (!(uu >= 0.0)) uu = 0.0;
     u64 y = (u64)floor(__dmul_rn(fmin(uu, 1.0), __ull2double_rn(total)));
     if (y >= total) y = total > 0 ? total - 1 : 0;
-    if (lead && total == 0) a.out_tokens[(size_t)b * T + s] = 0;  // only on rows without a finite logit
-    if (before <= y && y < before + own) {
-      u64 ra_ = before_a, rd_ = before_d, run = before;
+    if (lead && total == 0) out[s] = 0;  // only on rows without a finite logit
+    if (before <= y && y < before + sum) {
+      u64 run = before;
+#pragma unroll 1
       for (int i0 = s0; i0 < s1; i0 += 32) {
-        const u64 q = mass_at(i0 + lane, i0 + lane < s1, res, ra_, rd_);
-        const u64 cum = run + warp_scan(q, lane);
+        const u64 cum = run + warp_scan(i0 + lane < s1 ? mine[i0 - s0 + lane] : 0, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, cum > y);
         if (hit) {
-          if (lane == __ffs(hit) - 1) a.out_tokens[(size_t)b * T + s] = i0 + lane;
+          if (lane == __ffs(hit) - 1) out[s] = i0 + lane;
           break;
         }
         run = __shfl_sync(0xffffffffu, cum, 31);
@@ -591,18 +786,32 @@ __global__ void __launch_bounds__(kVThreads) verify_draw(const __grid_constant__
   cluster.sync();  // no CTA leaves while its shared memory is being read
 }
 
-// CTAs per row: the smallest power of two that gives every SM a block.
-int cluster_for(int rows, int n_sm) {
-  int c = 1;
-  while (c < kMaxCluster && static_cast<long long>(rows) * c < n_sm) c *= 2;
-  return c;
+// Sets a kernel's dynamic shared memory limit where a launch needs more than so far.
+template <typename K>
+cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<size_t> (&set)[kVerifyDevices]) {
+  if (bytes <= 28 * 1024) return cudaSuccess;  // beside up to 17 KB of static shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kVerifyDevices) return cudaErrorInvalidDevice;
+  if (bytes <= set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (bytes > set[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    set[dev].store(bytes, std::memory_order_release);
+  }
+  return cudaSuccess;
 }
 
 template <typename Args>
-cudaError_t launch(void (*kernel)(Args), int grid, int cluster, bool after, cudaStream_t st, const Args &args) {
+cudaError_t launch(void (*kernel)(Args), int grid, int cluster, int threads, size_t smem, cudaStream_t st,
+                   const Args &args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid) * cluster);
-  cfg.blockDim = dim3(kVThreads);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -612,8 +821,24 @@ cudaError_t launch(void (*kernel)(Args), int grid, int cluster, bool after, cuda
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = after ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+// CTAs per row.  A CTA's time goes with its logits (about 0.27 ns each, the fp64
+// exponentials of one SM), and the SMs hold ceil(rows C / n_sm) of them one after
+// another; a cluster's barriers cost about 4 us.
+int cluster_for(int rows, int V, int n_sm) {
+  int best = 1;
+  double least = 1e30;
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    const double us = 0.00027 * V / c * static_cast<double>((static_cast<long long>(rows) * c + n_sm - 1) / n_sm) + (c > 1 ? 4.0 : 0.0);
+    if (us < least) {
+      least = us;
+      best = c;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -621,10 +846,6 @@ cudaError_t launch(void (*kernel)(Args), int grid, int cluster, bool after, cuda
 size_t verify_sample_workspace(int B, int T) { return sizeof(RowStat) * static_cast<size_t>(B) * (2 * static_cast<size_t>(T) - 1); }
 
 cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
-  int dev = 0, n_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const int greedy = !(v.temperature > 0.0f);
   const double inv_t = greedy ? 0.0 : 1.0 / (double)v.temperature;
   const bool draft = v.draft_logits && !greedy;
@@ -638,7 +859,11 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   r.B = v.B;
   r.T = v.T;
   r.V = v.V;
-  const int cr = cluster_for(rows, n_sm);
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int cr = cluster_for(rows, v.V, n_sm);
   r.slice = ((v.V + cr - 1) / cr + 3) & ~3;
   r.vec4 = v.V % 4 == 0 && (reinterpret_cast<uintptr_t>(v.logits) & 15) == 0 &&
            (!draft || (reinterpret_cast<uintptr_t>(v.draft_logits) & 15) == 0);
@@ -646,9 +871,14 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   r.inv_t = inv_t;
   r.top_p = v.top_p;
   // masses are zero beyond max - l = 33 T; bins of equal width cover that range
-  r.bin_scale = greedy ? 0.f : static_cast<float>(kBins * inv_t / 33.0);
+  const double most = 3e38;  // a temperature near zero: still finite in fp32
+  r.bin_scale = greedy ? 0.f : static_cast<float>(std::min((kBins << kFine) * inv_t / 33.0, most));
+  r.inv_t2 = static_cast<float>(std::min(inv_t * 1.4426950408889634, most));  // log2(e)
   r.stats = stats;
-  e = launch(verify_rows, rows, cr, false, st, r);
+  static std::atomic<size_t> set_rows[kVerifyDevices];
+  const size_t smem_rows = sizeof(RowsShared) + sizeof(float) * kList;
+  e = allow_smem(verify_rows, smem_rows, set_rows);
+  if (e == cudaSuccess) e = launch(verify_rows, rows, cr, kVThreads, smem_rows, st, r);
   if (e != cudaSuccess) return e;
 
   DrawArgs d{};
@@ -659,14 +889,19 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   d.B = v.B;
   d.T = v.T;
   d.V = v.V;
-  const int cd = greedy ? 1 : cluster_for(v.B, n_sm);
-  d.slice = (v.V + cd - 1) / cd;
+  int cd = 1;
+  while (!greedy && cd < kMaxCluster && v.V > cd * 2 * kDrawThreads) cd *= 2;
+  d.per = ((v.V + cd * kDrawWarps - 1) / (cd * kDrawWarps) + 31) & ~31;
+  d.slice = d.per * kDrawWarps;
   d.greedy = greedy;
   d.inv_t = inv_t;
   d.stats = stats;
   d.out_tokens = v.out_tokens;
   d.out_accepted = v.out_accepted;
-  return launch(verify_draw, v.B, cd, true, st, d);
+  static std::atomic<size_t> set[kVerifyDevices];
+  const size_t smem = greedy ? 0 : sizeof(u64) * d.slice;
+  e = allow_smem(verify_draw, smem, set);
+  return e != cudaSuccess ? e : launch(verify_draw, v.B, cd, kDrawThreads, smem, st, d);
 }
 
 }  // namespace mk
