@@ -128,6 +128,7 @@ def lib():
         "mk_paged_attention_workspace": (u64, []),
         "mk_paged_attention": (i32, [kvp, vp, mk_strides, i32, i32, vp, vp, i32, i32, ctypes.c_float, vp, i32, vp,
                                      vp, u64, vp]),
+        "mk_decode_step_paged": (i32, [vp, vp, vp, i32, i32, kvp, vp, vp, vp]),
         "mk_verify_sample_workspace": (u64, [i32, i32]),
         "mk_verify_sample": (i32, [vp, vp, vp, i32, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, u64,
                                    vp]),
@@ -266,6 +267,12 @@ def mk_paged_attention(kv: mk_paged_kv, q: int, qs: mk_strides, dtype: int, n_q_
     """Attention of the newest rows over the pages (see include/mk.h)."""
     return lib().mk_paged_attention(ctypes.byref(kv), q, qs, dtype, n_q_heads, positions, counts, B, T, scale, rope,
                                     rope_len, out, workspace, workspace_bytes, stream)
+
+
+def mk_decode_step_paged(h, tokens: int, positions: int, B: int, T: int, layers, out_logits: Optional[int],
+                         out_argmax: int, stream: int) -> int:
+    """One step over a paged cache; layers: a ctypes array of mk_paged_kv (see include/mk.h)."""
+    return lib().mk_decode_step_paged(h, tokens, positions, B, T, layers, out_logits, out_argmax, stream)
 
 
 def mk_verify_sample_workspace(B: int, T: int) -> int:
@@ -681,6 +688,28 @@ class Decoder:
         return mk_decode_step_sample(self.h, tokens.data_ptr(), positions.data_ptr(), B, T, kv,
                                      _ptr(logits), temperature, top_p, _ptr(uniforms),
                                      out_tokens.data_ptr(), s.cuda_stream)
+
+    def step_paged(self, tokens, positions, B: int, T: int, layers: "Sequence[PagedKV]", logits, argmax,
+                   stream=None) -> int:
+        """One step over paged caches, one PagedKV per layer with a page table of
+        at least B rows.  Returns the launch status code."""
+        t = self._torch
+        _need(tokens, t.int32, B * T, "tokens")
+        dev = tokens.device
+        _need(positions, t.int32, B, "positions", dev)
+        if logits is not None:
+            _need(logits, t.float32, B * T * self.model.vocab, "logits", dev)
+        _need(argmax, t.int32, B * T, "argmax", dev)
+        if len(layers) != self.model.n_layers:
+            raise ValueError(f"layers: {len(layers)}, the model has {self.model.n_layers}")
+        for i, kv in enumerate(layers):
+            if kv.device != dev:
+                raise ValueError(f"layer {i}: on {kv.device}, expected {dev}")
+            if kv.page_table.shape[0] < B:
+                raise ValueError(f"layer {i}: a page table of {kv.page_table.shape[0]} sequences, {B} needed")
+        descs = (mk_paged_kv * len(layers))(*[kv.desc for kv in layers])
+        return _call_on(dev.index, mk_decode_step_paged, self.h, tokens.data_ptr(), positions.data_ptr(), B, T, descs,
+                        _ptr(logits), argmax.data_ptr(), _raw_stream(dev.index, stream))
 
     def steps_sample(self, tokens, positions, B: int, n_steps: int, k_cache, v_cache, logits,
                      temperature: float, top_p: float, uniforms, out_tokens, stream=None) -> int:

@@ -224,6 +224,7 @@ struct GraphEntry {
   uint64_t key[12];
   cudaGraphExec_t exec;
   int launches;  // kernels per replay
+  std::vector<mk_paged_kv> paged;  // paged steps: the layers' caches
 };
 
 struct mk_handle {
@@ -271,6 +272,7 @@ struct mk_handle {
   int32_t *sp_pos;  // the sampled multi-step loop's positions: [kv_capacity][min(max_seqs, 8)]
   int *w_count, *w_off, *w_pair_row, *w_pair_slot, *w_active;
   __nv_bfloat16 *w_xhi, *w_xlo, *w_ghi, *w_glo, *w_ahi, *w_alo, *w_shi, *w_slo;
+  void *w_paged = nullptr;  // workspace of the paged attention, zeroed
 };
 
 extern "C" {
@@ -520,6 +522,15 @@ MK_API int mk_create(const mk_model_desc *desc, const mk_weights *w, mk_handle *
     const int ld_max = std::max(std::max(QKVW, D), std::max(2 * Fs, std::max(d.n_experts, HD)));
     h->w_part_floats = 16LL * MR * ld_max;
     HALLOC(h->w_part, sizeof(float) * (size_t)h->w_part_floats);
+    {  // the paged step's attention; its counters start at zero
+      const size_t bytes = paged_attention_workspace(h->n_sm);
+      HALLOC(h->w_paged, bytes);
+      const cudaError_t ze = cudaMemset(h->w_paged, 0, bytes);
+      if (ze != cudaSuccess) {
+        mk_destroy(h);
+        return fail(MK_ERR_CUDA, "workspace setup failed: %s", cudaGetErrorString(ze));
+      }
+    }
     cudaError_t pe = wide_prepare();
     if (pe != cudaSuccess) {
       mk_destroy(h);
@@ -714,16 +725,34 @@ static void fill_wide(mk_handle *h, const int32_t *tokens, const int32_t *positi
   s.shi = h->w_shi; s.slo = h->w_slo;
 }
 
+// Whether a recorded graph was made for these layers (compared field by field: the
+// struct has no padding to trust).
+static bool same_layers(const std::vector<mk_paged_kv> &a, const std::vector<mk_paged_kv> &b) {
+  if (a.size() != b.size()) return false;
+  for (size_t i = 0; i < a.size(); ++i) {
+    const mk_paged_kv &x = a[i], &y = b[i];
+    if (x.k != y.k || x.v != y.v || x.k_scale != y.k_scale || x.v_scale != y.v_scale || x.page_table != y.page_table ||
+        x.n_pages != y.n_pages || x.page_size != y.page_size || x.max_pages != y.max_pages || x.dtype != y.dtype ||
+        x.n_kv_heads != y.n_kv_heads || x.head_dim != y.head_dim)
+      return false;
+  }
+  return true;
+}
+
+// paged: the layers' caches (host array [n_layers]) in place of kv, or NULL.
 static int run_wide(mk_handle *h, const int32_t *tokens, const int32_t *positions, int B, int T, mk_kv_cache kv,
-                    float *logits, int32_t *argmax, cudaStream_t stream) {
+                    const mk_paged_kv *paged, float *logits, int32_t *argmax, cudaStream_t stream) {
   const mk_model_desc &d = h->desc;
   if (!tokens || !positions || !argmax) return fail(MK_ERR_ARG, "tokens, positions and out_argmax are required");
-  if (!kv.k || !kv.v) return fail(MK_ERR_ARG, "kv.k and kv.v are required");
+  if (!paged && (!kv.k || !kv.v)) return fail(MK_ERR_ARG, "kv.k and kv.v are required");
   if (B > d.max_seqs || (long long)B * T > d.max_rows)
     return fail(MK_ERR_CAPACITY, "B=%d T=%d exceeds max_seqs=%d / max_rows=%d", B, T, d.max_seqs, d.max_rows);
   if (T > d.kv_capacity) return fail(MK_ERR_CAPACITY, "T=%d exceeds kv_capacity=%d", T, d.kv_capacity);
   WideStep s;
   fill_wide(h, tokens, positions, B, T, kv, logits, argmax, s);
+  s.paged = paged;
+  s.paged_ws = h->w_paged;
+  const std::vector<mk_paged_kv> layers(paged, paged ? paged + d.n_layers : nullptr);
   // The launch sequence is recorded once per (shape, buffers) into a CUDA graph
   // and replayed: a graph launch issues the ~300 kernels without a host call
   // each.  Graphs live in the handle's cache next to the multi-kernel ones.
@@ -737,10 +766,10 @@ static int run_wide(mk_handle *h, const int32_t *tokens, const int32_t *position
                             (uint64_t)(uintptr_t)kv.v,
                             (uint64_t)(uintptr_t)h->dbg_hidden,
                             (uint64_t)(uintptr_t)h->dbg_ids ^ (uint64_t)(uintptr_t)h->dbg_w,
-                            0,
+                            (uint64_t)layers.size(),
                             0};
   for (auto &g : h->graphs)
-    if (std::memcmp(g.key, key, sizeof key) == 0) {
+    if (std::memcmp(g.key, key, sizeof key) == 0 && same_layers(g.paged, layers)) {
       CUDA_TRY(cudaGraphLaunch(g.exec, stream));
       h->stats.graph_launches += 1;
       h->stats.kernel_launches += g.launches;
@@ -769,6 +798,7 @@ static int run_wide(mk_handle *h, const int32_t *tokens, const int32_t *position
   std::memcpy(ge.key, key, sizeof key);
   ge.exec = exec;
   ge.launches = launches;
+  ge.paged = layers;
   h->graphs.push_back(ge);
   CUDA_TRY(cudaGraphLaunch(exec, stream));
   h->stats.graph_launches += 1;
@@ -782,7 +812,7 @@ static int run_step(mk_handle *h, const int32_t *tokens, const int32_t *position
   if (!h) return fail(MK_ERR_ARG, "handle is NULL");
   if (B >= 1 && T >= 1 &&
       ((long long)B * T > kMaxRows || (h->variant == MK_TENSORCORE && (long long)B * T >= 2 && h->desc.n_experts > 0)))
-    return run_wide(h, tokens, positions, B, T, kv, logits, argmax, stream);
+    return run_wide(h, tokens, positions, B, T, kv, nullptr, logits, argmax, stream);
   Params p;
   Plan pl;
   int rc = fill_params(h, tokens, positions, B, T, kv, logits, argmax, p, pl);
@@ -980,6 +1010,25 @@ MK_API int mk_kv_gather(const mk_paged_kv *kv, const int32_t *starts, const int3
   a.vec = vec_ok(k, ks, out_dtype) && vec_ok(v, vs, out_dtype);
   CUDA_TRY(launch_kv_gather(a, out_dtype, static_cast<cudaStream_t>(stream)));
   return MK_OK;
+}
+
+MK_API int mk_decode_step_paged(mk_handle *h, const int32_t *tokens, const int32_t *positions, int32_t B, int32_t T,
+                                const mk_paged_kv *layers, float *out_logits, int32_t *out_argmax, void *stream) {
+  if (!h) return fail(MK_ERR_ARG, "handle is NULL");
+  const mk_model_desc &d = h->desc;
+  if (!layers) return fail(MK_ERR_ARG, "layers is NULL");
+  if (!h->w_paged || d.n_experts == 0)
+    return fail(MK_ERR_UNSUPPORTED, "a paged step needs a model with routed experts and a handle of max_rows >= 2");
+  if (B < 1 || T < 1) return fail(MK_ERR_ARG, "B and T must be >= 1");
+  for (int l = 0; l < d.n_layers; ++l) {
+    const int rc = check_paged_kv(&layers[l]);
+    if (rc) return rc;
+    if (layers[l].n_kv_heads != d.n_kv_heads || layers[l].head_dim != d.head_dim)
+      return fail(MK_ERR_ARG, "layer %d: the cache has %d heads of %d, the model %d of %d", l, layers[l].n_kv_heads,
+                  layers[l].head_dim, d.n_kv_heads, d.head_dim);
+  }
+  return run_wide(h, tokens, positions, B, T, mk_kv_cache{}, layers, out_logits, out_argmax,
+                  static_cast<cudaStream_t>(stream));
 }
 
 static int current_sm_count(int *n_sm) {

@@ -213,6 +213,9 @@ struct WideStep {
   int *count, *off, *pair_row, *pair_slot;
   int *active, *n_active;  // experts with rows, in increasing order, and how many
   __nv_bfloat16 *xhi, *xlo, *ghi, *glo, *ahi, *alo, *shi, *slo;
+  // a paged cache in place of kc and vc: host array [L], and its attention's workspace
+  const mk_paged_kv *paged;
+  void *paged_ws;
 };
 
 cudaError_t wide_prepare();

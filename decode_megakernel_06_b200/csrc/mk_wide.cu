@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <utility>
 
 #include "mk_internal.h"
@@ -472,6 +473,17 @@ __global__ void wide_kv_append(float *qkv, int W3, const int32_t *positions, int
     const float kr = i < half ? k[i] * cs.x - k[i + half] * cs.y : k[i] * cs.x + k[i - half] * cs.y;
     kc[base * hd + i] = __float2bfloat16_rn(kr);
     vc[base * hd + i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+// The paged attention's fp32 rows as the bf16 pair that the output projection takes.
+__global__ void wide_split_rows(const float *x, int n, __nv_bfloat16 *xhi, __nv_bfloat16 *xlo, int ldx) {
+  pdl_wait();
+  pdl_launch();
+  const int m = blockIdx.x;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    const long long at = static_cast<long long>(m) * ldx + c;
+    split_store(x[static_cast<long long>(m) * n + c], xhi + at, xlo + at);
   }
 }
 
@@ -1255,48 +1267,82 @@ cudaError_t wide_step(const WideStep &s, cudaStream_t st, int *launches) {
     ++n;
     Split sq{};
     WIDE_TRY(gemm(n, s, static_cast<const __nv_bfloat16 *>(lw.wqkv), nullptr, 1, W3, d, s.xhi, s.xlo, ldx, M, nullptr,
-                  nullptr, M, s.qkv, W3, 0, 0, s.part, st, &sq));
-    WIDE_TRY(launch(wide_kv_append, dim3(M, s.Hkv), dim3(256), 0, st, s.qkv, W3, s.positions_safe, s.T, s.Hq, s.Hkv, s.hd, s.rope, s.kc,
-                                                   s.vc, s.Bmax, s.cap, l, sq));
-    ++n;
-    {  // attention: chunk partials on the tensor cores, then the merge into the bf16 pair
-      const int G = s.Hq / s.Hkv, nch = (s.cap + kAcN - 1) / kAcN;
-      AttnArgs aa{};
-      // the kernel's TMA row coordinate is 32-bit
-      if (static_cast<uint64_t>(s.L) * s.Bmax * s.Hkv * s.cap > 0x7fffffffull ||
-          encode_2d_sw128(&aa.mk, s.kc, static_cast<uint64_t>(s.L) * s.Bmax * s.Hkv * s.cap, s.hd, s.hd, kAcN) != MK_OK)
-        return cudaErrorInvalidValue;
-      aa.qkv = s.qkv;
-      aa.W3 = W3;
-      aa.positions = s.positions_safe;
-      aa.T = s.T;
-      aa.Hq = s.Hq;
-      aa.Hkv = s.Hkv;
-      aa.rope = s.rope;
-      aa.vc = s.vc;
-      aa.Bmax = s.Bmax;
-      aa.cap = s.cap;
-      aa.layer = l;
-      aa.nch_max = nch;
-      aa.opart = s.attn_o;
-      aa.mlpart = s.attn_ml;
-      aa.error = s.error;
-      const int qn = s.T * G <= 16 ? 16 : kAcQ;  // N of the products: the group's query vectors
-      const dim3 grid(nch, s.B * s.Hkv, (s.T * G + qn - 1) / qn);
-      if (s.hd == 64 && qn == 16)
-        WIDE_TRY(launch(wide_attn_tc<64, 16>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(16), st, aa));
-      else if (s.hd == 64)
-        WIDE_TRY(launch(wide_attn_tc<64, 32>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(32), st, aa));
-      else if (qn == 16)
-        WIDE_TRY(launch(wide_attn_tc<128, 16>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(16), st, aa));
-      else
-        WIDE_TRY(launch(wide_attn_tc<128, 32>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(32), st, aa));
+                  nullptr, M, s.qkv, W3, 0, 0, s.part, st, s.paged ? nullptr : &sq));
+    if (s.paged) {  // the layer's pages: append, attention, and its rows for the output projection
+      const mk_strides qs{static_cast<int64_t>(s.T) * W3, W3, s.hd};
+      KvAppend ka{};
+      ka.kv = s.paged[l];
+      ka.k = s.qkv + s.Hq * s.hd;
+      ka.v = s.qkv + (s.Hq + s.Hkv) * s.hd;
+      ka.ks = ka.vs = qs;
+      ka.positions = s.positions_safe;
+      ka.B = s.B;
+      ka.T = s.T;
+      ka.rope = s.rope;
+      ka.rope_len = s.cap;
+      ka.vec = 1;
+      WIDE_TRY(launch_kv_append(ka, MK_F32, st));
       ++n;
-      // chunk groups per block: enough threads for long caches, few blocks' worth for short ones
-      const int mg = nch >= 32 ? kMgGroups : nch >= 16 ? 2 : 1;
-      WIDE_TRY(launch(wide_attn_merge, dim3(M, s.Hq), dim3(mg * s.hd), 0, st, s.positions_safe, s.T, s.Hq, s.Hkv, s.hd, nch, s.attn_o,
-                                                      s.attn_ml, s.xhi, s.xlo, ldx));
+      PagedAttn pa{};
+      pa.kv = s.paged[l];
+      pa.q = s.qkv;
+      pa.qs = qs;
+      pa.Hq = s.Hq;
+      pa.positions = s.positions_safe;
+      pa.B = s.B;
+      pa.T = s.T;
+      pa.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.hd)));
+      pa.rope = s.rope;
+      pa.rope_len = s.cap;
+      pa.out = s.attn_o;  // [M][Hq hd], within the partials' buffer
+      pa.vec = 1;
+      WIDE_TRY(launch_paged_attention(pa, MK_F32, s.paged_ws, s.n_sm, st));
       ++n;
+      WIDE_TRY(launch(wide_split_rows, dim3(M), dim3(256), 0, st, s.attn_o, HD, s.xhi, s.xlo, ldx));
+      ++n;
+    } else {
+      WIDE_TRY(launch(wide_kv_append, dim3(M, s.Hkv), dim3(256), 0, st, s.qkv, W3, s.positions_safe, s.T, s.Hq, s.Hkv, s.hd, s.rope, s.kc,
+                                                     s.vc, s.Bmax, s.cap, l, sq));
+      ++n;
+      {  // attention: chunk partials on the tensor cores, then the merge into the bf16 pair
+        const int G = s.Hq / s.Hkv, nch = (s.cap + kAcN - 1) / kAcN;
+        AttnArgs aa{};
+        // the kernel's TMA row coordinate is 32-bit
+        if (static_cast<uint64_t>(s.L) * s.Bmax * s.Hkv * s.cap > 0x7fffffffull ||
+            encode_2d_sw128(&aa.mk, s.kc, static_cast<uint64_t>(s.L) * s.Bmax * s.Hkv * s.cap, s.hd, s.hd, kAcN) != MK_OK)
+          return cudaErrorInvalidValue;
+        aa.qkv = s.qkv;
+        aa.W3 = W3;
+        aa.positions = s.positions_safe;
+        aa.T = s.T;
+        aa.Hq = s.Hq;
+        aa.Hkv = s.Hkv;
+        aa.rope = s.rope;
+        aa.vc = s.vc;
+        aa.Bmax = s.Bmax;
+        aa.cap = s.cap;
+        aa.layer = l;
+        aa.nch_max = nch;
+        aa.opart = s.attn_o;
+        aa.mlpart = s.attn_ml;
+        aa.error = s.error;
+        const int qn = s.T * G <= 16 ? 16 : kAcQ;  // N of the products: the group's query vectors
+        const dim3 grid(nch, s.B * s.Hkv, (s.T * G + qn - 1) / qn);
+        if (s.hd == 64 && qn == 16)
+          WIDE_TRY(launch(wide_attn_tc<64, 16>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(16), st, aa));
+        else if (s.hd == 64)
+          WIDE_TRY(launch(wide_attn_tc<64, 32>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(32), st, aa));
+        else if (qn == 16)
+          WIDE_TRY(launch(wide_attn_tc<128, 16>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(16), st, aa));
+        else
+          WIDE_TRY(launch(wide_attn_tc<128, 32>, dim3(grid), dim3(kAcThreads), attn_smem_bytes(32), st, aa));
+        ++n;
+        // chunk groups per block: enough threads for long caches, few blocks' worth for short ones
+        const int mg = nch >= 32 ? kMgGroups : nch >= 16 ? 2 : 1;
+        WIDE_TRY(launch(wide_attn_merge, dim3(M, s.Hq), dim3(mg * s.hd), 0, st, s.positions_safe, s.T, s.Hq, s.Hkv, s.hd, nch, s.attn_o,
+                                                        s.attn_ml, s.xhi, s.xlo, ldx));
+        ++n;
+      }
     }
     Split so{};
     WIDE_TRY(gemm(n, s, static_cast<const __nv_bfloat16 *>(lw.wo), nullptr, 1, d, HD, s.xhi, s.xlo, ldx, M, nullptr,

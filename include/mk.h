@@ -423,6 +423,22 @@ MK_API int mk_paged_attention(const mk_paged_kv *kv, const void *q, mk_strides q
                               const float *rope, int32_t rope_len, void *out, void *workspace,
                               uint64_t workspace_bytes, void *stream);
 
+/* mk_decode_step over a paged cache: each layer appends its keys and values with
+ * mk_kv_append and attends with mk_paged_attention (rows kept in fp32), on the
+ * tensor-core launch sequence of mk_wide blocks, for any block of up to max_rows rows.
+ *   layers     : HOST array of n_layers caches (read during the call), each with the
+ *                model's n_kv_heads and head_dim and a page table for the B
+ *                sequences; layers may share a table and mix types
+ *   the others : as mk_decode_step (positions[b] + T <= kv_capacity, the extent of the
+ *                handle's rotary table)
+ * Rows on unmapped pages are not kept, so map the pages of positions[b] .. positions[b]
+ * + T - 1 before the call.  The launches are recorded once per (shape, buffers,
+ * layers) as a CUDA graph and replayed.  A handle's steps must not overlap.
+ * Errors: MK_ERR_UNSUPPORTED (a dense model, or a handle of max_rows 1), and those
+ * of mk_decode_step and mk_kv_append. */
+MK_API int mk_decode_step_paged(mk_handle *h, const int32_t *tokens, const int32_t *positions, int32_t B, int32_t T,
+                                const mk_paged_kv *layers, float *out_logits, int32_t *out_argmax, void *stream);
+
 /* Bytes of the workspace of mk_verify_sample (no initial value needed; not
  * shared between calls that may overlap). */
 MK_API uint64_t mk_verify_sample_workspace(int32_t B, int32_t T);
