@@ -97,7 +97,7 @@ __device__ __forceinline__ void decode8(const uint2 &u, float (&x)[8]) {
 // rotary angles are held in registers, and the loads of several heads' rows are in
 // flight together.  A key row is rotated in fp32; then each value is rounded once:
 // to bf16, or to the e4m3 code of x / scale with scale = max(amax / 448, 2^-126)
-// over the row's finite values (half a step of e4m3, 2^-4 relative; the division
+// over the row's finite values (half a step of e4m3, 2^-4 relative; a true quotient
 // keeps x = amax on the largest code).  Every lane of a warp stays in the shuffles;
 // rows without a place are not written.  Bound by memory: each input byte is read
 // once, each cache byte written once.
@@ -149,18 +149,37 @@ __device__ __forceinline__ void put_row(void *pool, float *scales, long long row
   if constexpr (E4M3) {
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m = fabsf(x[i]);
-      amax = m < INFINITY ? fmaxf(amax, m) : amax;  // NaN compares false
-    }
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));  // NaN is passed over
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
+    const bool infinite = amax == INFINITY;
+    if (__any_sync(0xffffffffu, infinite)) {  // the largest finite value
+      float f = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f = fabsf(x[i]) < INFINITY ? fmaxf(f, fabsf(x[i])) : f;
+#pragma unroll
+      for (int o = kLanes / 2; o; o >>= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o, kLanes));
+      amax = f;
+    }
     const float scale = fmaxf(amax / kE4m3Max, kTinyScale);
+    // x / scale, correctly rounded: x r with r = 1 / scale, and its remainder once more
+    // (Markstein, Computation of elementary functions on the IBM RISC System/6000
+    // processor, 1990).  An infinity has no remainder.
+    const float r = __frcp_rn(scale);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = x[i] * r;
+      q[i] = fmaf(fmaf(-y, scale, x[i]), r, y);
+    }
+    if (infinite) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = fabsf(x[i]) == INFINITY ? x[i] : q[i];
+    }
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] / scale, x[2 * i + 1] / scale),
-                                                              __NV_SATFINITE, __NV_E4M3);
+      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
       w[i / 2] |= static_cast<uint32_t>(c) << (16 * (i & 1));
     }
     if (on) {

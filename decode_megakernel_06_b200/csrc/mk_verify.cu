@@ -35,7 +35,8 @@ constexpr int kMaxCluster = 8;
 constexpr double kMassScale = 70368744177664.0;  // 2^46
 constexpr int kBins = 1024;   // histogram bins over max - l
 constexpr int kFine = 10;     // each of 2^kFine fine ones: 2^20 in all, exact in fp32
-constexpr int kList = 8192;   // logits of the nucleus that a CTA keeps at hand
+constexpr int kQueue = 16;    // logits of the nucleus that a thread keeps at hand
+constexpr int kCache = 32768; // logits of a slice that are kept in shared memory where a nucleus is looked for
 constexpr int kCand = 512;    // tokens of the threshold's fine bin that the list holds
 constexpr int kVerifyDevices = 64;
 constexpr int kDrawThreads = 512;
@@ -63,10 +64,25 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+constexpr double kRound = 4503599627370496.0;  // 2^52: adding it rounds to a whole number
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A whole number x, 0 <= x < 2^52, from x + 2^52; zero from NaN.
+__device__ __forceinline__ u64 whole_bits(double x) {
+  const int hi = __double2hiint(x);
+  return hi < 0x43400000 ? __double_as_longlong(x) - 0x4330000000000000ll : 0;
+}
+
+// round_half_even(exp((l - m) / T) 2^46).  The product is exact, so its sum with 2^52 is
+// its rounding.  No test for masses that round to zero: a branch around the
+// exponential cost 20 of 65 cycles a warp.
 __device__ __forceinline__ u64 mass_of(float l, float m, double inv_t) {
-  const double z = ((double)l - (double)m) * inv_t;
-  // exp(-33) 2^46 < 0.5: the mass rounds to zero (NaN takes the other branch)
-  return z < -33.0 ? 0 : __double2ull_rn(exp(z) * kMassScale);
+  return whole_bits(fma(exp(((double)l - (double)m) * inv_t), kMassScale, kRound));
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -99,28 +115,28 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 struct RowsArgs {
   const float *logits, *draft;
   const int32_t *tokens;
-  int B, T, V, slice, vec4, greedy;
+  int B, T, V, slice, vec4, greedy, cached;
   double inv_t;
   float top_p, bin_scale, inv_t2;  // fine bins per unit of the logits; log2(e) / temperature
   RowStat *stats;  // [B * T] target rows, then [B * (T - 1)] draft rows
 };
 
-struct RowsShared {
+struct alignas(16) RowsShared {  // the queue and the cache behind it are read 16 bytes at a time
   uint32_t hist[kBins];       // read by the cluster
   u64 fine[1 << kFine];       // read by the cluster
-  u64 red[kVWarps];
-  float wmax[kVWarps], wsum[kVWarps];
-  uint32_t wkey[kVWarps];
-  u64 cta_sum, cta_sum2, cta_least;  // read by the cluster
-  float cta_max, cta_weight;
-  uint32_t cta_lo, cta_hi, n_cand;
+  u64 red[kVWarps], red2[kVWarps];
+  uint32_t wkey[kVWarps], wkey2[kVWarps];
+  u64 cta_sum, cta_sum2;  // read by the cluster
+  float cta_least;
+  uint32_t cta_key, cta_lo, cta_hi, n_cand;
   int32_t cta_id;
   u64 before, at_tau, same;
-  uint32_t tau, found, n_list;
+  uint32_t tau, found;
   int bin, last_bin;
   uint32_t cand_key[kCand], all_key[kCand];
   u64 cand_mass[kCand], all_mass[kCand];
 };
+static_assert(sizeof(RowsShared) % 16 == 0, "alignment of what follows");
 
 // The block's sum of v, in every thread.
 __device__ __forceinline__ u64 block_sum(u64 v, u64 *red, int lane, int warp) {
@@ -180,22 +196,23 @@ __device__ __forceinline__ void each(const float *src, int n, int vec4, int tid,
 }
 
 // One cluster per row (of one CTA where there are rows enough).  The row is read from
-// memory once and from L2 after that: for the largest logit (and an fp32 estimate of
-// the masses' sum), for the masses, and where a nucleus has to be found for its
-// tokens.  The masses, an fp64 exponential per logit, bound this kernel.
+// memory once and from L2 or shared memory after that: for the largest logit, for the
+// masses, and where a nucleus has to be found for its tokens.  The masses, an fp64
+// exponential per logit, bound this kernel.
 //
 // The nucleus: a token is left out if all tokens whose masses are no larger weigh no
 // more than Q - need, so one whose mass is below (Q - need) / V need not be counted.
-// The others go into a histogram over max - l, bins of equal width, in 32 bits with
-// the row's sum scaled to about 2^30: a guess of the threshold's bin, which the exact
-// sums of the next pass confirm or move.  That bin's tokens go into 1024 finer bins,
-// exactly, whose one holds the threshold: nearly always a single logit, perhaps of
-// many tokens; other keys in it are ranked.
+// The others go into a histogram over max - l, bins of equal width, of fp32 masses in
+// 32 bits: a guess of the threshold's bin, which the exact sums of the next pass
+// confirm or move.  That bin's tokens are ranked.  Where they are more than a list
+// holds, they first go into 1024 finer bins, exactly, whose one that holds the
+// threshold is nearly always a single logit of many tokens.
 __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constant__ RowsArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ __align__(16) unsigned char dyn[];
   RowsShared &sh = *reinterpret_cast<RowsShared *>(dyn);
-  float *list = reinterpret_cast<float *>(dyn + sizeof(RowsShared));  // [kList]
+  float *queue = reinterpret_cast<float *>(dyn + sizeof(RowsShared));  // [kQueue][kVThreads], then [kCache]
+  float *cache = queue + kQueue * kVThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = cluster.block_rank(), size = cluster.num_blocks();
   const int row = blockIdx.x / size;
@@ -205,53 +222,37 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
   const int lo = (int)rank * a.slice, n = max(0, min(a.slice, a.V - lo));
   const float *base = (is_draft ? a.draft : a.logits) + (size_t)r * a.V;
   const float *src = base + lo;
+  auto sync_all = [&] {
+    if (size > 1) cluster.sync();
+    else __syncthreads();
+  };
   const bool whole = a.top_p >= 1.0f;  // a nucleus is then hardly ever looked for
   pdl_wait();
   pdl_launch();
 
-  // ---- the largest logit; for a nucleus also about how much the masses weigh --------------
-  float mx = -INFINITY, wt = 0.f;
-  if (whole || a.greedy) {
-    each<4>(src, n, a.vec4, tid, [&](float x, int) { mx = fmaxf(mx, x); });
-  } else {
-    each<2>(src, n, a.vec4, tid, [&](float x, int) {
-      if (x > mx) {
-        wt *= exp2f((mx - x) * a.inv_t2);
-        mx = x;
-      }
-      wt += mx > -INFINITY ? exp2f((x - mx) * a.inv_t2) : 0.f;
+  // ---- the largest logit ---------------------------------------------------------------
+  float mx = -INFINITY;
+  if (a.cached) {
+    each<4>(src, n, a.vec4, tid, [&](float x, int i) {
+      if (i < n) cache[i] = x;
+      mx = fmaxf(mx, x);
     });
+  } else {
+    each<4>(src, n, a.vec4, tid, [&](float x, int) { mx = fmaxf(mx, x); });
   }
-  auto fold = [&](int width) {  // (mx, wt) over groups of `width` lanes
-    for (int o = width / 2; o; o >>= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, mx, o), ow = __shfl_xor_sync(0xffffffffu, wt, o);
-      const float to = fmaxf(mx, om);
-      wt = to == -INFINITY ? 0.f : wt * exp2f((mx - to) * a.inv_t2) + ow * exp2f((om - to) * a.inv_t2);
-      mx = to;
-    }
-  };
-  fold(32);
-  if (lane == 0) {
-    sh.wmax[warp] = mx;
-    sh.wsum[warp] = wt;
-  }
-  if (!whole)
-    for (int i = tid; i < kBins; i += kVThreads) sh.hist[i] = 0;
-  if (tid == 0) sh.n_list = sh.n_cand = 0;
+  uint32_t kmax = __reduce_max_sync(0xffffffffu, logit_key(mx));
+  if (lane == 0) sh.wkey[warp] = kmax;
+  sh.hist[tid] = 0;
+  if (tid == 0) sh.n_cand = 0;
   __syncthreads();
+  if (a.cached) src = cache;
   if (warp == 0) {
-    mx = sh.wmax[lane];
-    wt = sh.wsum[lane];
-    fold(32);
-    if (lane == 0) {
-      sh.cta_max = mx;
-      sh.cta_weight = wt;
-    }
+    kmax = __reduce_max_sync(0xffffffffu, sh.wkey[lane]);
+    if (lane == 0) sh.cta_key = kmax;
   }
-  cluster.sync();
-  mx = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_max, lane) : -INFINITY;
-  wt = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_weight, lane) : 0.f;
-  fold(32);
+  sync_all();
+  kmax = __reduce_max_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_key, lane) : 0u);
+  mx = key_logit(kmax);
   const float m = mx;
   const uint32_t gmax = logit_key(m);
 
@@ -267,68 +268,69 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
       const int v = __reduce_min_sync(0xffffffffu, static_cast<int>(sh.wkey[lane]));
       if (lane == 0) sh.cta_id = v;
     }
-    cluster.sync();
+    sync_all();
     if (rank == 0 && warp == 0) {
       const int v = __reduce_min_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_id, lane) : 0x7fffffff);
       if (lane == 0) a.stats[row].best = min(v, a.V - 1);
     }
-    cluster.sync();  // no CTA leaves while its shared memory is being read
+    sync_all();  // no CTA leaves while its shared memory is being read
     return;
   }
 
+  // The fine bin of a logit, rising as it falls (each step is monotone): the sum with 2^23
+  // rounds to a whole number, for less than a conversion costs.
   auto fine_of = [&](float v) {
-    return max((int)fminf((m - v) * a.bin_scale, (float)((kBins << kFine) - 1)), 0);
+    const float at = fminf(fmaxf((m - v) * a.bin_scale, 0.f), (float)((kBins << kFine) - 1));
+    return (int)(__float_as_uint(at + 8388608.f) - 0x4b000000u);
   };
-  // ---- the masses' sum and the smallest that is not zero; the guess' histogram ---------------
-  u64 sum = 0, least = ~0ull;
-  {
-    // weights are relative to the largest mass 2^46; wt < 2 kMaxVocab
-    const float up = 1073741824.0f / fmaxf(wt, 1.f);  // mass 2^46 in the histogram's unit
-    const double scale = (double)up / kMassScale;
-    const u64 skip = (u64)(0.99 * fmin(1.0, fmax(0.0, 1.0 - (double)a.top_p)) * (double)wt * kMassScale / a.V);
-    each<1>(src, n, a.vec4, tid, [&](float x, int) {
-      const u64 q = mass_of(x, m, a.inv_t);
-      sum += q;
-      if (q) least = min(least, q);
-      if (!whole && q > skip) atomicAdd(&sh.hist[fine_of(x) >> kFine], __double2uint_rn(__ull2double_rn(q) * scale));
-    });
+  // ---- the masses' sum and the smallest that is not zero -----------------------------------
+  u64 sum = 0;
+  float least = INFINITY;  // the smallest logit with a mass
+  each<1>(src, n, a.vec4, tid, [&](float x, int) {
+    const u64 q = mass_of(x, m, a.inv_t);
+    sum += q;
+    if (q) least = fminf(least, x);
+  });
+  sum = warp_sum(sum);
+  const uint32_t lk = __reduce_min_sync(0xffffffffu, logit_key(least));
+  if (lane == 0) {
+    sh.red[warp] = sum;
+    sh.wkey[warp] = lk;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-  sum = block_sum(sum, sh.red, lane, warp);
-  __syncthreads();
-  if (lane == 0) sh.red[warp] = least;
   __syncthreads();
   if (warp == 0) {
-    u64 v = sh.red[lane];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    sum = warp_sum(sh.red[lane]);
+    const uint32_t k = __reduce_min_sync(0xffffffffu, sh.wkey[lane]);
     if (lane == 0) {
       sh.cta_sum = sum;
-      sh.cta_least = v;
+      sh.cta_least = key_logit(k);
     }
   }
-  cluster.sync();
+  sync_all();
   const u64 total = cluster_total(cluster, &sh.cta_sum, size, lane);
-  u64 smallest = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_least, lane) : ~0ull;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) smallest = min(smallest, __shfl_xor_sync(0xffffffffu, smallest, o));
+  least = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_least, lane) : INFINITY;
+  least = key_logit(__reduce_min_sync(0xffffffffu, logit_key(least)));
+  const u64 smallest = least < INFINITY ? mass_of(least, m, a.inv_t) : ~0ull;
   const u64 need = nucleus_need(a.top_p, total);
 
   uint32_t tau = 0;       // every token with a mass
   u64 ties = 0, nucleus = total;
   bool cut = false;
   if (smallest <= total - need) {  // some token may be left out
-    // ---- the guess: the bin where the scaled sums reach need ------------------------------
+    // ---- the guess: the bin where fp32 masses, scaled to a sum of 2^22, reach need -----------
     // for top_p = 1 (fp64 rounded need below Q) at most 2^10 units are left out: the last bin with
     // a mass, or one shortly before it
-    int bin = min(kBins - 1, (int)((31.9 - log(__ull2double_rn(smallest))) * (kBins / 33.0)) + 1);
+    int bin = min((fine_of(least) >> kFine) + 1, kBins - 1);
     if (!whole) {
-      const uint32_t v = [&] {
-        uint32_t x = 0;
-        for (unsigned i = 0; i < size; ++i) x += cluster.map_shared_rank(&sh.hist[0], i)[tid];
-        return x;
-      }();
+      const float up = 4194304.f * (float)kMassScale / __ull2float_rn(total);  // a mass of 2^46
+      const float skip = 4194304.f * 0.99f * __ull2float_rn(total - need) / __ull2float_rn(total) / a.V;
+      each<2>(src, n, a.vec4, tid, [&](float x, int) {
+        const float w = ex2((x - m) * a.inv_t2) * up;
+        if (w > skip) atomicAdd(&sh.hist[fine_of(x) >> kFine], __float_as_uint(w + 8388608.f) - 0x4b000000u);
+      });
+      sync_all();
+      uint32_t v = 0;
+      for (unsigned i = 0; i < size; ++i) v += cluster.map_shared_rank(&sh.hist[0], i)[tid];
       static_assert(kBins == kVThreads && (1 << kFine) == kVThreads, "a thread per bin");
       uint32_t incl = v;
 #pragma unroll
@@ -345,134 +347,80 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
       uint32_t w = sh.wkey[lane];
       w = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
       incl += w;
-      const double want = __ull2double_rn(need) * (1073741824.0 / fmaxf(wt, 1.f)) / kMassScale;
-      if (v && (double)incl >= want) atomicMin(&sh.bin, tid);
+      const float want = 4194304.f * __ull2float_rn(need) / __ull2float_rn(total);
+      if (v && (float)incl >= want) atomicMin(&sh.bin, tid);
       if (v) atomicMax(&sh.last_bin, tid);
       __syncthreads();
       bin = min(sh.bin, sh.last_bin);
     }
     // ---- the exact sum above the bin and in it; the bin moves where the guess was off ---------
     u64 above = 0;
-    bool listed = false;
+    int queued = 0;      // this thread's logits up to the bin, in queue[k][tid]
+    bool listed = false;  // all of the CTA's are
 #pragma unroll 1
     for (int tries = 0; tries < kBins; ++tries) {
+      queued = 0;
       each<2>(src, n, a.vec4, tid, [&](float x, int i) {
-        const bool in = i < n && (fine_of(x) >> kFine) <= bin;
-        const unsigned hit = __ballot_sync(0xffffffffu, in);
-        uint32_t at = 0;
-        if (hit && lane == 0) at = atomicAdd(&sh.n_list, (uint32_t)__popc(hit));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1u));
-        if (in && at < kList) list[at] = x;
+        if (i < n && (fine_of(x) >> kFine) <= bin) {
+          if (queued < kQueue) queue[queued * kVThreads + tid] = x;
+          ++queued;
+        }
       });
-      __syncthreads();
-      listed = sh.n_list <= kList;
+      listed = !__syncthreads_or(queued > kQueue);
       u64 more = 0, in = 0;
       auto add = [&](float x, int i) {
         const int at = fine_of(x) >> kFine;
         if (i >= n || at > bin) return;
         const u64 q = mass_of(x, m, a.inv_t);
-        if (at < bin) more += q;
-        else in += q;
+        if (at < bin) {
+          more += q;
+        } else {
+          in += q;
+          const uint32_t c = atomicAdd(&sh.n_cand, 1u);
+          if (c < kCand) {
+            sh.cand_key[c] = logit_key(x);
+            sh.cand_mass[c] = q;
+          }
+        }
       };
       if (listed) {
 #pragma unroll 1
-        for (uint32_t k = tid; k < sh.n_list; k += kVThreads) add(list[k], 0);
+        for (int k = 0; k < queued; ++k) add(queue[k * kVThreads + tid], 0);
       } else {
         each<1>(src, n, a.vec4, tid, add);
       }
-      more = block_sum(more, sh.red, lane, warp);
-      in = block_sum(in, sh.red, lane, warp);
-      if (tid == 0) {
-        sh.cta_sum = more;
-        sh.cta_sum2 = in;
+      more = warp_sum(more);
+      in = warp_sum(in);
+      if (lane == 0) {
+        sh.red[warp] = more;
+        sh.red2[warp] = in;
       }
-      cluster.sync();
+      __syncthreads();
+      if (warp == 0) {
+        more = warp_sum(sh.red[lane]);
+        in = warp_sum(sh.red2[lane]);
+        if (lane == 0) {
+          sh.cta_sum = more;
+          sh.cta_sum2 = in;
+        }
+      }
+      sync_all();
       above = cluster_total(cluster, &sh.cta_sum, size, lane);
       const u64 inside = cluster_total(cluster, &sh.cta_sum2, size, lane);
       const bool up = above >= need && bin > 0, down = above + inside < need && bin < kBins - 1;
       if (!up && !down) break;
       bin += up ? -1 : 1;
-      cluster.sync();  // the sums have been read
-      if (tid == 0) sh.n_list = 0;
+      sync_all();  // the sums have been read
+      if (tid == 0) sh.n_cand = 0;
       __syncthreads();
     }
-    // f(l) for the bin's tokens in this CTA
-    auto of_bin = [&](auto f) {
-      if (listed) {
-#pragma unroll 1
-        for (uint32_t k = tid; k < sh.n_list; k += kVThreads)
-          if ((fine_of(list[k]) >> kFine) == bin) f(list[k]);
-      } else {
-        each<1>(src, n, a.vec4, tid, [&](float x, int i) {
-          if (i < n && (fine_of(x) >> kFine) == bin) f(x);
-        });
-      }
-    };
-    // ---- its fine bins, exactly -----------------------------------------------------------
-    sh.fine[tid] = 0;
-    __syncthreads();
-    of_bin([&](float x) {
-      const u64 q = mass_of(x, m, a.inv_t);
-      if (q) atomicAdd(&sh.fine[fine_of(x) & ((1 << kFine) - 1)], q);
-    });
-    cluster.sync();
-    u64 v = 0;
-    for (unsigned i = 0; i < size; ++i) v += cluster.map_shared_rank(&sh.fine[0], i)[tid];
-    u64 incl = warp_scan(v, lane);
-    if (lane == 31) sh.red[warp] = incl;
-    if (tid == 0) {  // kept only on non-finite input
-      sh.bin = 0;
-      sh.before = above;
-      sh.found = 0;
-      sh.n_cand = 0;
-    }
-    __syncthreads();
-    incl += above + warp_sum(lane < warp ? sh.red[lane] : 0);
-    if (incl - v < need && need <= incl) {
-      sh.bin = tid;
-      sh.before = incl - v;
-    }
-    __syncthreads();
-    const int fine = sh.bin | bin << kFine;
-    const u64 before = sh.before;
-    u64 at_tau = before, same = 0;
-    // ---- its tokens: one key, or a list of them to rank ------------------------------------------
-    uint32_t klo = 0xffffffffu, khi = 0;
-    of_bin([&](float x) {
-      if (fine_of(x) != fine) return;
-      const uint32_t key = logit_key(x);
-      klo = min(klo, key);
-      khi = max(khi, key);
-      const uint32_t at = atomicAdd(&sh.n_cand, 1u);
-      if (at < kCand) {
-        sh.cand_key[at] = key;
-        sh.cand_mass[at] = mass_of(x, m, a.inv_t);
-      }
-    });
-    klo = __reduce_min_sync(0xffffffffu, klo);
-    khi = __reduce_max_sync(0xffffffffu, khi);
-    if (lane == 0) sh.wkey[warp] = klo;
-    __syncthreads();
-    if (warp == 0) {
-      klo = __reduce_min_sync(0xffffffffu, sh.wkey[lane]);
-      if (lane == 0) sh.cta_lo = klo;
-    }
-    __syncthreads();
-    if (lane == 0) sh.wkey[warp] = khi;
-    __syncthreads();
-    if (warp == 0) {
-      khi = __reduce_max_sync(0xffffffffu, sh.wkey[lane]);
-      if (lane == 0) sh.cta_hi = khi;
-    }
-    cluster.sync();
-    klo = __reduce_min_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_lo, lane) : 0xffffffffu);
-    khi = __reduce_max_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_hi, lane) : 0u);
-    const uint32_t cnt = lane < (int)size ? *cluster.map_shared_rank(&sh.n_cand, lane) : 0u;
-    const uint32_t all = __reduce_add_sync(0xffffffffu, cnt);
-    if (klo == khi) {
-      tau = klo;
-      same = cluster_total(cluster, &sh.fine[fine & ((1 << kFine) - 1)], size, lane);
-    } else if (all <= kCand) {
+    // Ranks up to kCand listed tokens: tau is the key with sum(above it) < need <= sum(above
+    // it) + its ties' sum.  `before`: what is above all of them.
+    u64 at_tau = above, same = 0;
+    auto rank_listed = [&](u64 before) {
+      const uint32_t cnt = lane < (int)size ? *cluster.map_shared_rank(&sh.n_cand, lane) : 0u;
+      const uint32_t all = __reduce_add_sync(0xffffffffu, min(cnt, kCand + 1u));
+      if (all > kCand) return false;
       uint32_t first = cnt;
 #pragma unroll
       for (int o = 1; o < kMaxCluster; o <<= 1) {
@@ -480,17 +428,16 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
         if (lane >= o) first += w;
       }
       first -= cnt;  // entries of the CTAs before CTA `lane`
+#pragma unroll 1
       for (unsigned i = 0; i < size; ++i) {
         const uint32_t f = __shfl_sync(0xffffffffu, first, i), c = __shfl_sync(0xffffffffu, cnt, i);
-        const uint32_t *ck = cluster.map_shared_rank(sh.cand_key, i);
-        const u64 *cm = cluster.map_shared_rank(sh.cand_mass, i);
-        for (uint32_t k = tid; k < c; k += kVThreads) {
-          sh.all_key[f + k] = ck[k];
-          sh.all_mass[f + k] = cm[k];
+        if (tid < (int)c) {
+          sh.all_key[f + tid] = cluster.map_shared_rank(sh.cand_key, i)[tid];
+          sh.all_mass[f + tid] = cluster.map_shared_rank(sh.cand_mass, i)[tid];
         }
       }
+      if (tid == 0) sh.found = 0;
       __syncthreads();
-      // tau is the key with sum(above it) < need <= sum(above it) + its ties' sum
       if (tid < (int)all) {
         const uint32_t key = sh.all_key[tid];
         u64 over = before, tied = 0;
@@ -509,37 +456,117 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
         }
       }
       __syncthreads();
-      if (sh.found) {
+      if (sh.found) {  // always, on finite input
         tau = sh.tau;
         at_tau = sh.at_tau;
         same = sh.same;
       }
-    } else {
-      // More than the list holds, and not one key: the keys between klo and khi are halved
-      // until one is left, the largest with sum(keys >= it) >= need.
-      auto sum_from = [&](uint32_t key, bool only) {
-        u64 part = 0;
-        of_bin([&](float x) {
-          const uint32_t k = logit_key(x);
-          if (fine_of(x) == fine && (only ? k == key : k >= key)) part += mass_of(x, m, a.inv_t);
+      return true;
+    };
+    // f(l) for the bin's tokens in this CTA
+    auto of_bin = [&](auto f) {
+      if (listed) {
+#pragma unroll 1
+        for (int k = 0; k < queued; ++k) {
+          const float x = queue[k * kVThreads + tid];
+          if ((fine_of(x) >> kFine) == bin) f(x);
+        }
+      } else {
+        each<1>(src, n, a.vec4, tid, [&](float x, int i) {
+          if (i < n && (fine_of(x) >> kFine) == bin) f(x);
         });
-        part = block_sum(part, sh.red, lane, warp);
-        cluster.sync();  // cta_sum has been read
-        if (tid == 0) sh.cta_sum = part;
-        cluster.sync();
-        return cluster_total(cluster, &sh.cta_sum, size, lane);
-      };
-      while (klo < khi) {
-        const uint32_t mid = klo + (khi - klo + 1) / 2;
-        if (before + sum_from(mid, false) >= need) klo = mid;
-        else khi = mid - 1;
       }
-      tau = klo;
-      at_tau = before + sum_from(tau, false);
-      same = sum_from(tau, true);
-      at_tau -= same;
+    };
+    if (!rank_listed(above)) {
+      // ---- many tokens in the bin: its fine bins, exactly -----------------------------------
+      sh.fine[tid] = 0;
+      __syncthreads();
+      of_bin([&](float x) {
+        const u64 q = mass_of(x, m, a.inv_t);
+        if (q) atomicAdd(&sh.fine[fine_of(x) & ((1 << kFine) - 1)], q);
+      });
+      sync_all();
+      u64 v = 0;
+      for (unsigned i = 0; i < size; ++i) v += cluster.map_shared_rank(&sh.fine[0], i)[tid];
+      u64 incl = warp_scan(v, lane);
+      if (lane == 31) sh.red[warp] = incl;
+      if (tid == 0) {  // kept only on non-finite input
+        sh.bin = 0;
+        sh.before = above;
+        sh.n_cand = 0;
+      }
+      __syncthreads();
+      incl += above + warp_sum(lane < warp ? sh.red[lane] : 0);
+      if (incl - v < need && need <= incl) {
+        sh.bin = tid;
+        sh.before = incl - v;
+      }
+      __syncthreads();
+      const int fine = sh.bin | bin << kFine;
+      const u64 before = sh.before;
+      at_tau = before;
+      // ---- its tokens: one key, or a list of them to rank --------------------------------------
+      uint32_t klo = 0xffffffffu, khi = 0;
+      of_bin([&](float x) {
+        if (fine_of(x) != fine) return;
+        const uint32_t key = logit_key(x);
+        klo = min(klo, key);
+        khi = max(khi, key);
+        const uint32_t at = atomicAdd(&sh.n_cand, 1u);
+        if (at < kCand) {
+          sh.cand_key[at] = key;
+          sh.cand_mass[at] = mass_of(x, m, a.inv_t);
+        }
+      });
+      klo = __reduce_min_sync(0xffffffffu, klo);
+      khi = __reduce_max_sync(0xffffffffu, khi);
+      if (lane == 0) {
+        sh.wkey[warp] = klo;
+        sh.wkey2[warp] = khi;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        klo = __reduce_min_sync(0xffffffffu, sh.wkey[lane]);
+        khi = __reduce_max_sync(0xffffffffu, sh.wkey2[lane]);
+        if (lane == 0) {
+          sh.cta_lo = klo;
+          sh.cta_hi = khi;
+        }
+      }
+      sync_all();
+      klo = __reduce_min_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_lo, lane) : 0xffffffffu);
+      khi = __reduce_max_sync(0xffffffffu, lane < (int)size ? *cluster.map_shared_rank(&sh.cta_hi, lane) : 0u);
+      if (klo == khi) {
+        tau = klo;
+        same = cluster_total(cluster, &sh.fine[fine & ((1 << kFine) - 1)], size, lane);
+      } else if (!rank_listed(before)) {
+        // More than the list holds, and not one key: the keys between klo and khi are halved
+        // until one is left, the largest with sum(keys >= it) >= need.
+        auto sum_from = [&](uint32_t key, bool only) {
+          u64 part = 0;
+          of_bin([&](float x) {
+            const uint32_t k = logit_key(x);
+            if (fine_of(x) == fine && (only ? k == key : k >= key)) part += mass_of(x, m, a.inv_t);
+          });
+          part = block_sum(part, sh.red, lane, warp);
+          sync_all();  // cta_sum has been read
+          if (tid == 0) sh.cta_sum = part;
+          sync_all();
+          return cluster_total(cluster, &sh.cta_sum, size, lane);
+        };
+#pragma unroll 1
+        while (klo < khi) {
+          const uint32_t mid = klo + (khi - klo + 1) / 2;
+          if (before + sum_from(mid, false) >= need) klo = mid;
+          else khi = mid - 1;
+        }
+        tau = klo;
+        at_tau = before + sum_from(tau, false);
+        same = sum_from(tau, true);
+        at_tau -= same;
+      }
     }
-    cluster.sync();  // cta_sum is written again below
+    sync_all();  // lists have been read, cta_sum is written again below
     u64 q_tau = mass_of(key_logit(tau), m, a.inv_t);
     if (q_tau == 0) q_tau = 1;  // only on non-finite input
     ties = need > at_tau ? (need - at_tau + q_tau - 1) / q_tau : 1;
@@ -560,7 +587,7 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
       each<2>(src, n, a.vec4, tid, [&](float y, int i) { lower += logit_key(y) == tau && i < n && lo + i < d; });
       lower = block_sum(lower, sh.red, lane, warp);
       if (tid == 0) sh.cta_sum = lower;
-      cluster.sync();
+      sync_all();
       if (cluster_total(cluster, &sh.cta_sum, size, lane) < ties) drafted = mass_of(l, m, a.inv_t);
     }
   }
@@ -573,7 +600,7 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
     o.tau = tau;
     o.cut = cut;
   }
-  cluster.sync();  // no CTA leaves while its shared memory is being read
+  sync_all();  // no CTA leaves while its shared memory is being read
 }
 
 struct DrawArgs {
@@ -593,9 +620,12 @@ struct RowMass {
   u64 ties;
   double inv_t;
   bool cut;
-  __device__ __forceinline__ u64 of(float l, u64 tied) const {
+  // + 2^52: a whole number, see whole_bits
+  __device__ __forceinline__ double of(float l, u64 tied) const {
     const uint32_t key = logit_key(l);
-    return key > tau || (key == tau && (!cut || tied < ties)) ? mass_of(l, m, inv_t) : 0;
+    const bool in = key > tau || (key == tau && (!cut || tied < ties));
+    const double q = fma(exp(((double)l - (double)m) * inv_t), kMassScale, kRound);
+    return in ? q : kRound;
   }
 };
 
@@ -717,33 +747,33 @@ __global__ void __launch_bounds__(kDrawThreads) verify_draw(const __grid_constan
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + 32 * k + lane;
-        va[k] = i < s1 ? la[i] : -INFINITY;
+        va[k] = i < s1 ? la[i] : -INFINITY;  // no mass
         vd[k] = two && i < s1 ? ld[i] : -INFINITY;
       }
-#pragma unroll 1
+#pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + 32 * k + lane;
         if (i0 + 32 * k >= s1) break;
-        const float l = va[k], y = vd[k];
         u64 na = ta, nd = td;
         if (cut) {
-          const unsigned ea = __ballot_sync(0xffffffffu, i < s1 && logit_key(l) == A.tau);
-          const unsigned ed = __ballot_sync(0xffffffffu, two && i < s1 && logit_key(y) == D.tau);
+          const unsigned ea = __ballot_sync(0xffffffffu, i < s1 && logit_key(va[k]) == A.tau);
+          const unsigned ed = __ballot_sync(0xffffffffu, two && i < s1 && logit_key(vd[k]) == D.tau);
           na += __popc(ea & ((1u << lane) - 1u));
           nd += __popc(ed & ((1u << lane) - 1u));
           ta += __popc(ea);
           td += __popc(ed);
         }
-        u64 q = i < s1 ? A.of(l, na) : 0;
+        double q = A.of(va[k], na);
         if (two) {
-          const u64 w = i < s1 ? D.of(y, nd) : 0;
-          const u64 p = __double2ull_rn(__dmul_rn(__ull2double_rn(q), ra)), o = __double2ull_rn(__dmul_rn(__ull2double_rn(w), rd));
-          q = p > o ? p - o : 0;
+          // each share rounded to a whole number, as its mass times 2^46 / sum
+          const double p = __dadd_rn(__dmul_rn(q - kRound, ra), kRound), o = __dadd_rn(__dmul_rn(D.of(vd[k], nd) - kRound, rd), kRound);
+          q = p > o ? kRound + (p - o) : kRound;
         } else if (res && i == x) {
-          q = 0;
+          q = kRound;
         }
-        if (i < s1) mine[i - s0] = q;
-        sum += q;
+        const u64 w = whole_bits(q);
+        if (i < s1) mine[i - s0] = w;
+        sum += w;
       }
     }
     sum = warp_sum(sum);
@@ -876,7 +906,9 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   r.inv_t2 = static_cast<float>(std::min(inv_t * 1.4426950408889634, most));  // log2(e)
   r.stats = stats;
   static std::atomic<size_t> set_rows[kVerifyDevices];
-  const size_t smem_rows = sizeof(RowsShared) + sizeof(float) * kList;
+  r.cached = !greedy && v.top_p < 1.0f && r.slice <= kCache;
+  const size_t smem_rows = sizeof(RowsShared) + (greedy ? 0 : sizeof(float) * kQueue * kVThreads) +
+                           (r.cached ? sizeof(float) * kCache : 0);
   e = allow_smem(verify_rows, smem_rows, set_rows);
   if (e == cudaSuccess) e = launch(verify_rows, rows, cr, kVThreads, smem_rows, st, r);
   if (e != cudaSuccess) return e;
