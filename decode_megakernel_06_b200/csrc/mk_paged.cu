@@ -765,6 +765,13 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         }
       }
     };
+    // a unit's rows on their way into L2: lanes 0 .. 15 a key row each, the others a value row
+    auto prefetch = [&](int row) {
+      if (row < 0) return;
+      const char *src = static_cast<const char *>(lane < 16 ? a.kv.k : a.kv.v) + static_cast<long long>(row) * (HD * X::kBytes);
+#pragma unroll
+      for (int i = 0; i < HD * X::kBytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
+    };
     int row = row_at(seg0 + warp), next = row_at(seg0 + warp + kAtWarps);
 
     // ---- Q: rotated, in pieces, in the layout of the product's B operand -----------------
@@ -796,6 +803,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       }
       load_k(row);  // the first unit's loads wait for its page's number; the rows' are on their way
       load_v(row);
+      prefetch(next);
       float x[kQuads][4], y[kQuads][4];
 #pragma unroll
       for (int i = 0; i < kQuads; ++i)
@@ -876,6 +884,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
     }
     for (int unit = seg0 + warp; unit < seg1; unit += kAtWarps) {
       const int after = row_at(unit + 2 * kAtWarps);
+      prefetch(after);
       const int p0 = unit * kUnit;
       // S^T = K Q^T, one sum per piece of q while there are few tiles: the chains of
       // dependent products are shorter
