@@ -378,9 +378,9 @@ struct AtShape {
   // blocks, which leave fewer items cut and overlap one's prologue with another's
   // loop (27 us against 34 in blocks of 12 warps, 32 ragged sequences); with more
   // rows in one block, whose join has half as many parts and twice the threads.
-  static constexpr int kWarps = NT == 1 ? 4 : 8;
+  static constexpr int kWarps = NT <= 2 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kBlocks = NT == 1 ? 3 : 1;
+  static constexpr int kBlocks = NT == 1 || (NT == 2 && (E4M3 || HD == 64)) ? 3 : NT == 2 ? 2 : 1;
   static constexpr int NQ = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int NP = sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int kQBytes = Geo<HD, E4M3>::KS * NQ * NT * 32 * 8;      // fragments of Q^T
@@ -433,7 +433,7 @@ struct AttnArgs {
   PagedAttn a;
   int G, R, n_rg;            // query heads of a KV head, rows of a KV head, row groups
   int vec;                   // rows of q start on 16-byte boundaries
-  int few;                   // up to 32 sequences of one row group each, units below 2^31
+  int few;                   // up to 32 sequences of up to 8 row groups each, units below 2^31
   Div by_page, by_G;
   int cap;                   // positions of a page table's row
   float qscale;              // scale * log2(e)
@@ -628,14 +628,22 @@ __device__ __noinline__ Place place_of_many(const AttnArgs &p, int rows, long lo
   return w;
 }
 
-// Up to 32 sequences of one row group each: every warp counts for itself.
+// Up to 32 sequences of a few row groups each: every warp counts for itself.
 __device__ __forceinline__ Place place_of_few(const AttnArgs &p, int rows) {
   const int lane = threadIdx.x & 31, hkv = p.a.kv.n_kv_heads, grid = gridDim.x;
-  const int units = lane < p.a.B ? units_of(group_len(p, rows, lane, 0)) : 0;
-  int line = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units * hkv)));
+  auto seq_weight = [&](int size) {
+    int n = 0;
+    if (lane < p.a.B) {
+#pragma unroll 1
+      for (int rg = 0; rg < p.n_rg; ++rg) n += weight_of(units_of(group_len(p, rows, lane, rg)), size);
+    }
+    return n * hkv;
+  };
+  int n = seq_weight(1);
+  int line = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
   Place w{};
-  w.size = part_size(line, p.a.B * hkv, grid);
-  const int n = weight_of(units, w.size) * hkv;
+  w.size = part_size(line, p.a.B * p.n_rg * hkv, grid);
+  if (w.size > 1) n = seq_weight(w.size);
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1298,18 +1306,18 @@ cudaError_t launch_kv_gather(const KvGather &args, int out_dtype, cudaStream_t s
 constexpr size_t kCountBytes = sizeof(uint32_t) * 3 * kAtMaxBlocks;
 
 size_t paged_attention_workspace(int n_sm) {
-  // two parts of 32 rows in a block per SM: more than 3 blocks of 8 rows or one of 16
-  return kCountBytes + sizeof(float) * 2 * static_cast<size_t>(n_sm) * 32 * (128 + 2);
+  // two parts of 16 rows in 3 blocks per SM: more than of 8 rows
+  return kCountBytes + sizeof(float) * 2 * static_cast<size_t>(n_sm) * 48 * (128 + 2);
 }
 
 template <int HD, typename TIO, bool E4M3, int NT>
 static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStream_t st) {
   using S = AtShape<HD, TIO, E4M3, NT>;
-  static_assert(S::kBlocks * S::kRows <= 32 && HD <= 128, "workspace");
+  static_assert(S::kBlocks * S::kRows <= 48 && HD <= 128, "workspace");
   const int blocks = std::min(n_sm * S::kBlocks, kAtMaxBlocks);
   p.n_rg = (p.R + S::kRows - 1) / S::kRows;
-  p.few = p.a.B <= 32 && p.n_rg == 1 &&
-          static_cast<long long>(p.a.B) * p.a.kv.n_kv_heads * (p.cap / kUnit + 1) < (1ll << 31);
+  p.few = p.a.B <= 32 && p.n_rg <= 8 &&
+          static_cast<long long>(p.a.B) * p.n_rg * p.a.kv.n_kv_heads * (p.cap / kUnit + 1) < (1ll << 31);
   p.count = static_cast<uint32_t *>(workspace);
   p.part = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + kCountBytes);
   p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD / 4);
@@ -1330,8 +1338,7 @@ static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStr
 template <int HD, typename TIO, bool E4M3>
 static cudaError_t run_rows(AttnArgs &p, void *workspace, int n_sm, cudaStream_t st) {
   if (p.R <= 8) return run_attention<HD, TIO, E4M3, 1>(p, workspace, n_sm, st);
-  if (p.R <= 16) return run_attention<HD, TIO, E4M3, 2>(p, workspace, n_sm, st);
-  return run_attention<HD, TIO, E4M3, 4>(p, workspace, n_sm, st);
+  return run_attention<HD, TIO, E4M3, 2>(p, workspace, n_sm, st);
 }
 
 static Div div_by(uint32_t d) {  // d < 2^31: exact for dividends below 2^31 (Granlund and Montgomery 1994)
