@@ -341,15 +341,23 @@ __global__ void __launch_bounds__(kRowThreads) kv_gather(const __grid_constant__
 // first product's layout into the second's by movmatrix.  Loads go straight from
 // memory into registers, a whole unit (8 KB of a bf16 cache) at a time per warp.
 //
-// Exactness.  bf16 rows and codes are exact operands.  A query value enters as
-// NQ pieces (bf16 cache: 3 truncated bf16 pieces are the fp32 value itself; codes:
-// 2 fp16 pieces of the row divided by a power of two, 2^-24 of the value), a
-// weight as 3 truncated bf16 pieces, again the value itself; with bf16 rows in and
-// out two pieces (2^-16 of it) are well under the output's rounding of 2^-8.
-// Everything else is fp32.
+// Exactness.  bf16 rows are exact operands, and so are codes in fp16.  With a bf16
+// cache a query value and a weight enter as 3 truncated bf16 pieces, which are the
+// fp32 value itself; with bf16 rows in and out as two (2^-17 of it), well under the
+// output's rounding of 2^-8.  With codes they enter as 2 fp16 pieces, 2^-24 of the
+// value: queries of the row divided by a power of two, weights times their value's
+// scale under a reference that keeps them below 2^14.  Everything else is fp32.
 // ---------------------------------------------------------------------------
 constexpr int kUnit = 16;          // positions per unit
-constexpr float kLazy = 8.0f;      // a score may pass its row's reference by 2^8 before it is moved
+// A score may pass its row's reference by 2^kLazy before the reference is moved (fewer
+// moves, and no maximum to find in most units).  In an 8-bit cache the weights times
+// their values' scales enter the second product in fp16, so the reference follows the
+// scores plus log2(scale): a product is set to 2^kBase at most and may grow to 2^14.
+template <bool E4M3>
+struct Lazy {
+  static constexpr float kLazy = E4M3 ? 14.0f : 8.0f, kBase = E4M3 ? 6.0f : 0.0f;
+};
+constexpr float kLeastScale = -80.0f;  // log2 of scales below it counts as this: the sums of weights stay finite
 constexpr int kMinUnits = 8;       // units per block, at least
 constexpr int kLongShare = 64;     // units per block from which items are cut anywhere
 constexpr int kJoin = 32;          // blocks of an item joined by one; more are joined in two levels
@@ -382,7 +390,7 @@ struct AtShape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kBlocks = NT == 1 || (NT == 2 && (E4M3 || HD == 64)) ? 3 : NT == 2 ? 2 : 1;
   static constexpr int NQ = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
-  static constexpr int NP = sizeof(TIO) == 4 ? 3 : 2;
+  static constexpr int NP = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int kQBytes = Geo<HD, E4M3>::KS * NQ * NT * 32 * 8;      // fragments of Q^T
   static constexpr int kLdq = HD + 4;                                       // row stride of the rotated q
   static constexpr int kStage = kRows * kLdq * 4;
@@ -473,23 +481,23 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
   return y;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// Two e4m3 codes (low 16 bits) to fp16x2, and that to bf16x2 (both exact).
+// Two e4m3 codes (low 16 bits) to fp16x2: exact.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t pair) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t f16_bf16(uint32_t h) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t *>(&b);
-}
-
 // The pair (x, y) as N bf16x2 words whose values add up to it: truncated pieces for
 // N = 3 (all 24 bits), a rounded and a rounded rest for N = 2 (2^-17).
 template <int N>
@@ -935,12 +943,13 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
           for (int i = kSums - 2; i >= 0; --i) s[n][j] += sp[i][n][j];
         }
-      float ks_[2] = {1.f, 1.f}, vs_[2] = {1.f, 1.f};
+      float ks_[2] = {1.f, 1.f}, vs_[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
       if constexpr (E4M3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           ks_[i] = __shfl_sync(0xffffffffu, ksc, g + 8 * i);
           vs_[i] = __shfl_sync(0xffffffffu, vsc, g + 8 * i);
+          lv[i] = fmaxf(lg2(fabsf(vs_[i])), kLeastScale);
         }
       }
       load_k(next);  // in flight through the softmax and the second product
@@ -965,17 +974,18 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) over = over || s[n][j] > m[n][j & 1] + kLazy;
+        for (int j = 0; j < 4; ++j) over = over || s[n][j] > m[n][j & 1] + (Lazy<E4M3>::kLazy - lv[j >> 1]);
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x = fmaxf(s[n][j], s[n][j + 2]);
+            // an infinite scale of a masked position gives NaN, which fmaxf passes over
+            float x = fmaxf(s[n][j] + lv[0], s[n][j + 2] + lv[1]);
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float to = fmaxf(m[n][j], x);
+            const float to = fmaxf(m[n][j], x - Lazy<E4M3>::kBase);
             const float by = to == -INFINITY ? 1.f : ex2(m[n][j] - to);
             m[n][j] = to;
             l[n][j] *= by;
@@ -1027,7 +1037,8 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t w[NP];
-          split_bf16<NP>(s[n][2 * i], s[n][2 * i + 1], w);
+          if constexpr (E4M3) split_f16(s[n][2 * i], s[n][2 * i + 1], w);
+          else split_bf16<NP>(s[n][2 * i], s[n][2 * i + 1], w);
 #pragma unroll
           for (int k = 0; k < NP; ++k) pb[n][k][i] = turn8x8(w[k]);
         }
@@ -1037,10 +1048,10 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         if constexpr (E4M3) {
           const uint32_t sel = t & 1 ? 0x7362 : 0x5140;  // codes 2 t, 2 t + 1 of both positions
           const uint32_t x = __byte_perm(vw[0][t / 2], vw[1][t / 2], sel), y = __byte_perm(vw[2][t / 2], vw[3][t / 2], sel);
-          a0 = f16_bf16(codes_f16(x & 0xffffu));
-          a1 = f16_bf16(codes_f16(x >> 16));
-          a2 = f16_bf16(codes_f16(y & 0xffffu));
-          a3 = f16_bf16(codes_f16(y >> 16));
+          a0 = codes_f16(x & 0xffffu);
+          a1 = codes_f16(x >> 16);
+          a2 = codes_f16(y & 0xffffu);
+          a3 = codes_f16(y >> 16);
         } else {
           a0 = __byte_perm(vw[0][t], vw[1][t], 0x5410);
           a1 = __byte_perm(vw[0][t], vw[1][t], 0x7632);
@@ -1050,7 +1061,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
         for (int k = 0; k < NP; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma<false>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+          for (int n = 0; n < NT; ++n) mma<E4M3>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
       }
       load_v(next);  // in flight through the next first product
       row = next;
