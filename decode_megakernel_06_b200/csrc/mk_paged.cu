@@ -1058,10 +1058,24 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           a2 = __byte_perm(vw[2][t], vw[3][t], 0x5410);
           a3 = __byte_perm(vw[2][t], vw[3][t], 0x7632);
         }
+        if constexpr (sizeof(TIO) == 4) {
+          // The tensor cores' fp32 sums truncate: kept in them over a long cache they fell
+          // behind by 7e-6 of the output (128k positions).  So each unit's is its own, and
+          // added with rounding.
 #pragma unroll
-        for (int k = 0; k < NP; ++k)
+          for (int n = 0; n < NT; ++n) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma<E4M3>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+            for (int k = NP - 1; k >= 0; --k) mma<E4M3>(d, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][n][j] += d[j];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma<E4M3>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+        }
       }
       load_v(next);  // in flight through the next first product
       row = next;

@@ -74,8 +74,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // A whole number x, 0 <= x < 2^52, from x + 2^52; zero from NaN.
 __device__ __forceinline__ u64 whole_bits(double x) {
-  const int hi = __double2hiint(x);
-  return hi < 0x43400000 ? __double_as_longlong(x) - 0x4330000000000000ll : 0;
+  return static_cast<unsigned>(__double2hiint(x)) < 0x43400000u ? __double_as_longlong(x) - 0x4330000000000000ll : 0;
 }
 
 // round_half_even(exp((l - m) / T) 2^46).  The product is exact, so its sum with 2^52 is
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
   uint32_t tau = 0;       // every token with a mass
   u64 ties = 0, nucleus = total;
   bool cut = false;
-  if (smallest <= total - need) {  // some token may be left out
+  if (total > 0 && smallest <= total - need) {  // some token may be left out
     // ---- the guess: the bin where fp32 masses, scaled to a sum of 2^22, reach need -----------
     // for top_p = 1 (fp64 rounded need below Q) at most 2^10 units are left out: the last bin with
     // a mass, or one shortly before it

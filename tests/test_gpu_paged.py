@@ -214,6 +214,32 @@ def test_attention_long_split(kind):
     assert torch.equal(first, again)
 
 
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_attention_long_sums_do_not_drift(kind):
+    """100k positions in fp32: each term's error is its own, so the output's is that of a
+    term, not of the sum: 8 u for a weight (score, exponential, pieces), 8 u for the
+    sums' own roundings and the truncation within a unit."""
+    n, page, hd, hq, hkv = 100_000, 64, 128, 16, 4
+    g = torch.Generator(device=DEV).manual_seed(31)
+    pages = -(-n // page)
+    k, v = (torch.randn((pages, hkv, page, hd), generator=g, device=DEV) for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    if kind == BF16:
+        kv = mk.PagedKV(k.to(BF16), v.to(BF16), table)
+        kk, vv = kv.k.double(), kv.v.double()
+    else:
+        sk, sv = k.abs().amax(-1) / 448, v.abs().amax(-1) / 448
+        kv = mk.PagedKV((k / sk[..., None]).to(E4M3), (v / sv[..., None]).to(E4M3), table, sk, sv)
+        kk, vv = kv.k.double() * sk.double()[..., None], kv.v.double() * sv.double()[..., None]
+    q = torch.randn((1, 1, hq, hd), generator=g, device=DEV)
+    out = torch.empty_like(q)
+    assert kv.attention(q, torch.tensor([n - 1], dtype=torch.int32, device=DEV), out, mk.paged_attention_workspace(q.device)) == mk.MK_OK
+    for h in range(hkv):
+        a, b = kk[:, h].reshape(-1, hd)[:n], vv[:, h].reshape(-1, hd)[:n]
+        ref = torch.softmax(q[0, 0, 4 * h:4 * h + 4].double() @ a.T * hd ** -0.5, -1) @ b
+        assert float((out[0, 0, 4 * h:4 * h + 4].double() - ref).norm() / ref.norm()) <= 16 * U
+
+
 def test_attention_many_sequences():
     lens = [1 + (37 * i) % 90 for i in range(700)]
     c = Cache(lens, 2, 64, 16, BF16, seed=6)

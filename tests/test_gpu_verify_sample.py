@@ -134,6 +134,22 @@ def test_banned_tokens():
     assert not ((out >= 100) & (out < 700)).any()
 
 
+def test_rows_that_are_not_finite():
+    """Out of contract: some token of the vocabulary, and the other blocks as ever."""
+    lg, dr, tok, u = block(8, 3, 900, 12)
+    want = gpu(lg, dr, tok, 1.0, 0.9, u)
+    bad = lg.copy()
+    bad[0, :, 5], bad[1, :], bad[2, :, 7], bad[3, :] = np.nan, np.nan, np.inf, -np.inf
+    dbad = dr.copy()
+    dbad[4, :, 5], dbad[5, :] = np.nan, -np.inf
+    for t, p in ((1.0, 0.9), (1.0, 1.0), (0.0, 1.0)):
+        out, acc = gpu(bad, dbad, tok, t, p, u)
+        for b in range(8):
+            assert 1 <= acc[b] <= 3 and ((out[b, :acc[b]] >= 0) & (out[b, :acc[b]] < 900)).all(), (t, p, b, out[b])
+        if (t, p) == (1.0, 0.9):
+            assert (out[6:] == want[0][6:]).all() and (acc[6:] == want[1][6:]).all()
+
+
 def test_drafts_outside_the_vocabulary():
     lg, dr, tok, u = block(4, 5, 600, 3)
     tok[0, 1], tok[1, 3], tok[2, 4], tok[3, 2] = -1, 600, 2 ** 31 - 1, -2 ** 31

@@ -104,3 +104,20 @@ def _tensors(**kw):
 def test_tensor_refusals(kw):
     with pytest.raises(ValueError):
         _tensors(**kw)
+
+
+def test_calls_make_their_device_current_and_put_the_other_back(monkeypatch):
+    now, seen = [2], []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "set_device", lambda i: now.__setitem__(0, i))
+
+    def call(x):
+        seen.append(now[0])
+        if x is None:
+            raise RuntimeError("within the call")
+        return x
+
+    assert mk._call_on(2, call, 5) == 5 and mk._call_on(1, call, 6) == 6 and now == [2]
+    with pytest.raises(RuntimeError):
+        mk._call_on(0, call, None)
+    assert now == [2] and seen == [2, 1, 0]
