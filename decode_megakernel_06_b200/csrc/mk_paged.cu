@@ -4,9 +4,8 @@
 //
 // A pool is [page][KV head][slot][head_dim]; position p of sequence b is slot
 // p % page_size of page table[b][p / page_size].  A row of head_dim values is
-// handled by head_dim / 8 lanes of 8 consecutive values each: 16 bytes of a bf16
-// row, 8 of an e4m3 row, so that a row's bytes are read and written by
-// neighbouring lanes in whole sectors.
+// appended by head_dim / 16 lanes and gathered by head_dim / 8, neighbouring lanes
+// reading and writing neighbouring bytes in whole sectors.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -91,163 +90,235 @@ __device__ __forceinline__ void decode8(const uint2 &u, float (&x)[8]) {
   }
 }
 
+// Four consecutive values of a row, kept in their own type until they are used.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 v;
+  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float *p, int vec) {
+    if (vec) v = *reinterpret_cast<const float4 *>(p);
+    else v = make_float4(p[0], p[1], p[2], p[3]);
+  }
+  __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void clear() { v = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int vec) {
+    if (vec) {
+      v = *reinterpret_cast<const uint2 *>(p);
+    } else {
+      const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+      v = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+
 // ---------------------------------------------------------------------------
-// Append.  A group of HD / 8 lanes takes a token of sequence blockIdx.y and every
+// Append.  A group of HD / 16 lanes takes a token of sequence blockIdx.y and every
 // `spread`-th of its KV heads: the place of the token is looked up once, its
-// rotary angles are held in registers, and the loads of several heads' rows are in
-// flight together.  A key row is rotated in fp32; then each value is rounded once:
+// rotary angles are held in registers, and the next head's rows are in flight while
+// one's are rounded.  Sixteen values a lane: what is done once per row and lane (the
+// largest value, its scale, a reciprocal, addresses) is most of the instructions.  A key row is rotated in fp32; then each value is rounded once:
 // to bf16, or to the e4m3 code of x / scale with scale = max(amax / 448, 2^-126)
 // over the row's finite values (half a step of e4m3, 2^-4 relative; a true quotient
 // keeps x = amax on the largest code).  Every lane of a warp stays in the shuffles;
 // rows without a place are not written.  Bound by memory: each input byte is read
 // once, each cache byte written once.
 // ---------------------------------------------------------------------------
-constexpr int kHeadsAtOnce = 2;  // heads whose key and value rows a group loads together
+constexpr int kHeadsAtOnce = 2;  // heads whose key and value rows a group of a gather loads together
 
-// Eight values of a row in their own type.
+// Eight consecutive values of a row in their own type.
 template <typename T>
-struct Eight;
-template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p, int vec) {
-    if (vec) {
-      a = *reinterpret_cast<const float4 *>(p);
-      b = *reinterpret_cast<const float4 *>(p + 4);
+struct Eight {
+  Four<T> lo, hi;
+  __device__ __forceinline__ void clear() {
+    lo.clear();
+    hi.clear();
+  }
+  __device__ __forceinline__ void load(const T *p, int vec) {
+    if (sizeof(T) == 2 && vec) {  // one 16-byte load
+      const uint4 u = *reinterpret_cast<const uint4 *>(p);
+      set(u);
     } else {
-      a = make_float4(p[0], p[1], p[2], p[3]);
-      b = make_float4(p[4], p[5], p[6], p[7]);
+      lo.load(p, vec);
+      hi.load(p + 4, vec);
     }
   }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-};
-template <>
-struct Eight<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int vec) {
-    if (vec) {
-      u = *reinterpret_cast<const uint4 *>(p);
-    } else {
-      const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
-      u = make_uint4(q[0] | static_cast<uint32_t>(q[1]) << 16, q[2] | static_cast<uint32_t>(q[3]) << 16,
-                     q[4] | static_cast<uint32_t>(q[5]) << 16, q[6] | static_cast<uint32_t>(q[7]) << 16);
+  __device__ __forceinline__ void set(const uint4 &u) {
+    if constexpr (sizeof(T) == 2) {
+      lo.v = make_uint2(u.x, u.y);
+      hi.v = make_uint2(u.z, u.w);
     }
   }
-  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8(u, x); }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return i < 2 ? make_float2(lo.at(2 * i), lo.at(2 * i + 1)) : make_float2(hi.at(2 * i - 4), hi.at(2 * i - 3));
+  }
 };
 
-// Rounds a row's eight values of this lane and writes them to row `row` of a pool.
+// Two fp32 values in one instruction: appending an 8-bit cache is bound by issue slots.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long &>(d))
+      : "l"(reinterpret_cast<const unsigned long long &>(a)), "l"(reinterpret_cast<const unsigned long long &>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long &>(d))
+      : "l"(reinterpret_cast<const unsigned long long &>(a)), "l"(reinterpret_cast<const unsigned long long &>(b)),
+        "l"(reinterpret_cast<const unsigned long long &>(c)));
+  return d;
+}
+
+// Rounds a row and writes it at dst (its scale at *scale_at): a lane holds dimensions
+// 8 lane .. 8 lane + 7 in x[0 .. 3] and HD / 2 + 8 lane .. in x[4 .. 7].
 template <int HD, bool E4M3>
-__device__ __forceinline__ void put_row(void *pool, float *scales, long long row, bool on, const float (&x)[8], int lane8) {
-  constexpr int kLanes = HD / 8;
-  const long long at = row * HD + 8 * lane8;
+__device__ __forceinline__ void put_row(char *dst, float *scale_at, bool on, float2 (&x)[8], int lane) {
+  constexpr int kLanes = HD / 16;
   if constexpr (E4M3) {
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));  // NaN is passed over
+    for (int i = 0; i < 8; ++i) amax = fmaxf(fmaxf(amax, fabsf(x[i].x)), fabsf(x[i].y));  // NaN is passed over
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
-    const bool infinite = amax == INFINITY;
-    if (__any_sync(0xffffffffu, infinite)) {  // the largest finite value
+    if (__any_sync(0xffffffffu, amax == INFINITY)) {  // the largest finite value; infinities get its code
       float f = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f = fabsf(x[i]) < INFINITY ? fmaxf(f, fabsf(x[i])) : f;
+      for (int i = 0; i < 8; ++i) {
+        f = fabsf(x[i].x) < INFINITY ? fmaxf(f, fabsf(x[i].x)) : f;
+        f = fabsf(x[i].y) < INFINITY ? fmaxf(f, fabsf(x[i].y)) : f;
+      }
 #pragma unroll
       for (int o = kLanes / 2; o; o >>= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o, kLanes));
       amax = f;
+      const float most = fmaxf(f, kE4m3Max * kTinyScale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i].x = fabsf(x[i].x) == INFINITY ? copysignf(most, x[i].x) : x[i].x;
+        x[i].y = fabsf(x[i].y) == INFINITY ? copysignf(most, x[i].y) : x[i].y;
+      }
     }
-    const float scale = fmaxf(amax / kE4m3Max, kTinyScale);
-    // x / scale, correctly rounded: x r with r = 1 / scale, and its remainder once more
-    // (Markstein, Computation of elementary functions on the IBM RISC System/6000
-    // processor, 1990).  An infinity has no remainder.
+    // Quotients a / b, correctly rounded: y = a r with r = 1 / b, and its remainder once
+    // more, y + r (a - y b) (Markstein, Computation of elementary functions on the IBM
+    // RISC System/6000 processor, 1990).
+    constexpr float k448 = 1.0f / kE4m3Max;
+    const float s0 = amax * k448;
+    const float scale = fmaxf(fmaf(fmaf(-s0, kE4m3Max, amax), k448, s0), kTinyScale);
     const float r = __frcp_rn(scale);
-    float q[8];
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-scale, -scale);
+    float2 q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float y = x[i] * r;
-      q[i] = fmaf(fmaf(-y, scale, x[i]), r, y);
+      const float2 y = mul2(x[i], r2);
+      q[i] = fma2(fma2(y, s2, x[i]), r2, y);
     }
-    if (infinite) {
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = fabsf(x[i]) == INFINITY ? x[i] : q[i];
-    }
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-      w[i / 2] |= static_cast<uint32_t>(c) << (16 * (i & 1));
-    }
+    for (int i = 0; i < 4; ++i)
+      w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q[2 * i], __NV_SATFINITE, __NV_E4M3)) |
+             static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q[2 * i + 1], __NV_SATFINITE, __NV_E4M3)) << 16;
     if (on) {
-      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = make_uint2(w[0], w[1]);
-      if (lane8 == 0) scales[row] = scale;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(dst + HD / 2) = make_uint2(w[2], w[3]);
+      if (lane == 0) *scale_at = scale;
     }
   } else if (on) {
-    store8(static_cast<__nv_bfloat16 *>(pool) + at, 1, x);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[i].x, x[i].y);
+      w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(dst + HD) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
 template <int HD, typename TIn, bool E4M3>
-__global__ void __launch_bounds__(kRowThreads) kv_append(const __grid_constant__ KvAppend a) {
+__global__ void __launch_bounds__(kRowThreads, 2) kv_append(const __grid_constant__ KvAppend a) {
   pdl_wait();
   pdl_launch();
-  constexpr int kLanes = HD / 8;
-  const int lane8 = threadIdx.x % kLanes, hkv = a.kv.n_kv_heads;
+  constexpr int kLanes = HD / 16;
+  const int lane = threadIdx.x % kLanes, hkv = a.kv.n_kv_heads;
   const int group = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes;
   const int t = group / a.spread, h0 = group - t * a.spread;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const long long p = static_cast<long long>(a.positions[b]) + t;
-    bool on = t < a.T && (!a.counts || t < a.counts[b]) && (!a.rope || p < a.rope_len);
-    const int first = on ? pool_row(a.kv, b, 0, p) : -1;  // the row of head 0
-    on = first >= 0;
+    bool on = t < a.T && (!a.counts || t < a.counts[b]);
     if (!__any_sync(0xffffffffu, on)) continue;
-    float2 cs[8];
+    const long long p = static_cast<long long>(a.positions[b]) + t;
+    // this group's next rows to load; read before their place is known
+    const long long k_step = a.ks.head * a.spread, v_step = a.vs.head * a.spread;
+    const TIn *k = static_cast<const TIn *>(a.k) + b * a.ks.seq + t * a.ks.token + h0 * a.ks.head + 8 * lane;
+    const TIn *v = static_cast<const TIn *>(a.v) + b * a.vs.seq + t * a.vs.token + h0 * a.vs.head + 8 * lane;
+    const bool has_row = on;
+    using Raw = Eight<TIn>[2][2];  // key and value, lower and upper half
+    auto load = [&](Raw &raw, int h) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        raw[0][half].clear();
+        raw[1][half].clear();
+        if (has_row && h < hkv) {
+          raw[0][half].load(k + half * (HD / 2), a.vec);
+          raw[1][half].load(v + half * (HD / 2), a.vec);
+        }
+      }
+      k += k_step;
+      v += v_step;
+    };
+    Raw raw;
+    load(raw, h0);
+    on = on && (!a.rope || p < a.rope_len);
+    const int first = on ? pool_row(a.kv, b, 0, p) : -1;  // the row of head 0
+    // (cos, cos) and (sin, sin) of this lane's pairs of dimensions i, i + HD / 2
+    float2 cos2[4], sin2[4];
     if (a.rope) {
-      const float2 *src = a.rope + (on ? p * (HD / 2) : 0) + 8 * (lane8 % (kLanes / 2));
+      const float2 *src = a.rope + (on && p >= 0 ? p * (HD / 2) : 0) + 8 * lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] = src[i];
-      if (lane8 < kLanes / 2) {  // the sine's sign of a row's lower half
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i].y = -cs[i].y;
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = src[2 * i], w = src[2 * i + 1];
+        cos2[i] = make_float2(u.x, w.x);
+        sin2[i] = make_float2(u.y, w.y);
       }
     }
-    const TIn *k = static_cast<const TIn *>(a.k) + b * a.ks.seq + t * a.ks.token + 8 * lane8;
-    const TIn *v = static_cast<const TIn *>(a.v) + b * a.vs.seq + t * a.vs.token + 8 * lane8;
-    for (int hb = 0; hb < hkv; hb += kHeadsAtOnce * a.spread) {  // as often in every lane
-      Eight<TIn> rk[kHeadsAtOnce], rv[kHeadsAtOnce];
+    on = first >= 0;
+    // where this group's next row goes
+    constexpr int kBytes = E4M3 ? 1 : 2;
+    long long row = first + static_cast<long long>(h0) * a.kv.page_size;
+    const long long row_step = static_cast<long long>(a.spread) * a.kv.page_size;
+    char *kd = static_cast<char *>(a.kv.k) + (row * HD + 8 * lane) * kBytes;
+    char *vd = static_cast<char *>(a.kv.v) + (row * HD + 8 * lane) * kBytes;
+    for (int hb = 0; hb < hkv; hb += a.spread) {  // as often in every lane
+      const int h = hb + h0;
+      const bool put = on && h < hkv;
+      float2 x[2][8];
 #pragma unroll
-      for (int i = 0; i < kHeadsAtOnce; ++i) {
-        const int h = hb + h0 + i * a.spread;
-        rk[i].clear();
-        rv[i].clear();
-        if (on && h < hkv) {
-          rk[i].load(k + h * a.ks.head, a.vec);
-          rv[i].load(v + h * a.vs.head, a.vec);
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[kv][j] = raw[kv][j / 4].pair(j % 4);
+      load(raw, h + a.spread);  // in flight through this turn's rounding
+      if (a.rope) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 lo = x[0][j], hi = x[0][j + 4], minus = make_float2(-sin2[j].x, -sin2[j].y);
+          x[0][j] = fma2(hi, minus, mul2(lo, cos2[j]));
+          x[0][j + 4] = fma2(lo, sin2[j], mul2(hi, cos2[j]));
         }
       }
-#pragma unroll
-      for (int i = 0; i < kHeadsAtOnce; ++i) {
-        const int h = hb + h0 + i * a.spread;
-        if (!__any_sync(0xffffffffu, h < hkv)) break;
-        const bool put = on && h < hkv;
-        const long long row = first + static_cast<long long>(h) * a.kv.page_size;
-        float x[8];
-        rk[i].get(x);
-        if (a.rope) {  // value j turns with j + HD / 2, which the lane HD / 16 away holds
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float other = __shfl_xor_sync(0xffffffffu, x[j], kLanes / 2, kLanes);
-            x[j] = x[j] * cs[j].x + other * cs[j].y;
-          }
-        }
-        put_row<HD, E4M3>(a.kv.k, a.kv.k_scale, row, put, x, lane8);
-        rv[i].get(x);
-        put_row<HD, E4M3>(a.kv.v, a.kv.v_scale, row, put, x, lane8);
-      }
+      put_row<HD, E4M3>(kd, a.kv.k_scale + row, put, x[0], lane);
+      put_row<HD, E4M3>(vd, a.kv.v_scale + row, put, x[1], lane);
+      row += row_step;
+      kd += row_step * (HD * kBytes);
+      vd += row_step * (HD * kBytes);
     }
   }
 }
@@ -397,37 +468,6 @@ struct AtShape {
   static constexpr int kLd = HD + 4;                                        // row stride of the warps' sums
   static constexpr int kMerge = kWarps * kRows * kLd * 4;
   static constexpr int kSmem = kMerge > kQBytes + kStage ? kMerge : kQBytes + kStage;
-};
-
-// Four consecutive values of a row, kept in their own type until they are used.
-template <typename T>
-struct Four;
-template <>
-struct Four<float> {
-  float4 v;
-  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void load(const float *p, int vec) {
-    if (vec) v = *reinterpret_cast<const float4 *>(p);
-    else v = make_float4(p[0], p[1], p[2], p[3]);
-  }
-  __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-};
-template <>
-struct Four<__nv_bfloat16> {
-  uint2 v;
-  __device__ __forceinline__ void clear() { v = make_uint2(0, 0); }
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int vec) {
-    if (vec) {
-      v = *reinterpret_cast<const uint2 *>(p);
-    } else {
-      const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
-      v = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    const uint32_t w = i < 2 ? v.x : v.y;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-  }
 };
 
 struct Div {  // x / d = (x magic) >> shift for 0 <= x < 2^31
@@ -1284,8 +1324,8 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
 
 // Groups per token and the grid: heads of a token are spread over groups while
 // there are too few tokens to fill the GPU (about 64 groups of an SM).
-dim3 row_grid(const mk_paged_kv &kv, int B, int T, int &spread) {
-  const int per = kRowThreads / (kv.head_dim / 8);
+dim3 row_grid(const mk_paged_kv &kv, int lanes, int B, int T, int &spread) {
+  const int per = kRowThreads / lanes;
   const long long tokens = static_cast<long long>(B) * T, want = 148 * 64;
   spread = static_cast<int>(std::max(1ll, std::min<long long>(kv.n_kv_heads, want / tokens)));
   const unsigned groups = static_cast<unsigned>(T) * spread;  // checked to fit by the caller
@@ -1296,7 +1336,7 @@ dim3 row_grid(const mk_paged_kv &kv, int B, int T, int &spread) {
 
 cudaError_t launch_kv_append(const KvAppend &args, int in_dtype, cudaStream_t st) {
   KvAppend a = args;
-  const dim3 grid = row_grid(a.kv, a.B, a.T, a.spread), block(kRowThreads);
+  const dim3 grid = row_grid(a.kv, a.kv.head_dim / 16, a.B, a.T, a.spread), block(kRowThreads);
   const bool f32 = in_dtype == MK_F32, e4m3 = a.kv.dtype == MK_E4M3;
   if (a.kv.head_dim == 64) {
     if (f32) return e4m3 ? launch(kv_append<64, float, true>, grid, block, 0, st, a)
@@ -1312,7 +1352,7 @@ cudaError_t launch_kv_append(const KvAppend &args, int in_dtype, cudaStream_t st
 
 cudaError_t launch_kv_gather(const KvGather &args, int out_dtype, cudaStream_t st) {
   KvGather a = args;
-  const dim3 grid = row_grid(a.kv, a.B, a.T, a.spread), block(kRowThreads);
+  const dim3 grid = row_grid(a.kv, a.kv.head_dim / 8, a.B, a.T, a.spread), block(kRowThreads);
   const bool f32 = out_dtype == MK_F32, e4m3 = a.kv.dtype == MK_E4M3;
   if (a.kv.head_dim == 64) {
     if (f32) return e4m3 ? launch(kv_gather<64, float, true>, grid, block, 0, st, a)
