@@ -398,7 +398,7 @@ class PagedKV:
                                 n_pages, page, page_table.shape[1], heads, hd, kinds[k.dtype])
         self._index, self._batch, self._heads, self._hd = self.device.index, page_table.shape[0], heads, hd
         self._kinds = {torch.float32: MK_F32, torch.bfloat16: MK_BF16}
-        self._int = torch.int32
+        self._int, self._byte = torch.int32, torch.uint8
 
     def _rows(self, t, name: str, heads: Optional[int]):
         """Checks a [B, T, heads, head_dim] operand (fp32 or bf16, any strides but a
@@ -434,12 +434,14 @@ class PagedKV:
         """The rotary table's pointer and number of positions (None, 0 without one)."""
         if rope is None:
             return None, 0
-        import torch
+        shape = rope.shape
+        if (self._kinds.get(rope.dtype) != MK_F32 or len(shape) != 3 or shape[1] != self._hd // 2 or shape[2] != 2
+                or shape[0] < 1 or not rope.is_contiguous() or rope.get_device() != self._index):
+            import torch
 
-        _need(rope, torch.float32, 1, "rope", self.device, dims=3)
-        if rope.shape[1] != self._hd // 2 or rope.shape[2] != 2:
-            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, {self._hd // 2}, 2]")
-        return rope.data_ptr(), rope.shape[0]
+            _need(rope, torch.float32, 1, "rope", self.device, dims=3)
+            raise ValueError(f"rope: shape {tuple(shape)}, expected [positions, {self._hd // 2}, 2]")
+        return rope.data_ptr(), shape[0]
 
     def append(self, k, v, positions, counts=None, rope=None, stream=None) -> int:
         """mk_kv_append: rows k, v [B, T, n_kv_heads, head_dim] at positions[b] + t
@@ -469,16 +471,15 @@ class PagedKV:
         """mk_paged_attention: rows q [B, T, n_q_heads, head_dim] at positions[b] + t
         over the cache, into out (contiguous, like q); scale defaults to
         1 / sqrt(head_dim).  ``workspace`` is paged_attention_workspace's."""
-        import torch
-
         shape, st, kind = self._rows(q, "q", None)
-        _need(out, q.dtype, 1, "out", self.device, dims=4)
-        if out.shape != shape:
+        if out.dtype != q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != self._index:
+            _need(out, q.dtype, 1, "out", self.device, dims=4)
             raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(shape)}")
         pos = self._ints(positions, "positions")
         cnt = None if counts is None else self._ints(counts, "counts")
         table, n = self._rope(rope)
-        _need(workspace, torch.uint8, 1, "workspace", self.device)
+        if workspace.dtype != self._byte or not workspace.is_contiguous() or workspace.get_device() != self._index:
+            _need(workspace, self._byte, 1, "workspace", self.device)
         if scale is None:
             scale = self._hd ** -0.5
         return _call_on(self._index, mk_paged_attention, self.desc, q.data_ptr(), mk_strides(st[0], st[1], st[2]),
