@@ -31,12 +31,11 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 // The pool row of position p of sequence b, head h, or -1 where it has none
 // (negative, past the table, unmapped page).
 __device__ __forceinline__ int pool_row(const mk_paged_kv &kv, int b, int h, long long p) {
-  if (p < 0) return -1;
-  const long long e = p / kv.page_size;
-  if (e >= kv.max_pages) return -1;
+  if (p < 0 || p >= static_cast<long long>(kv.max_pages) * kv.page_size) return -1;
+  const int at = static_cast<int>(p), e = at / kv.page_size;  // below 2^31, as checked by the caller
   const int page = kv.page_table[static_cast<long long>(b) * kv.max_pages + e];
   if (page < 0 || page >= kv.n_pages) return -1;
-  return (page * kv.n_kv_heads + h) * kv.page_size + static_cast<int>(p - e * kv.page_size);
+  return (page * kv.n_kv_heads + h) * kv.page_size + (at - e * kv.page_size);
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
@@ -430,7 +429,7 @@ struct Lazy {
 };
 constexpr float kLeastScale = -80.0f;  // log2 of scales below it counts as this: the sums of weights stay finite
 constexpr int kMinUnits = 8;       // units per block, at least
-constexpr int kLongShare = 64;     // units per block from which items are cut anywhere
+constexpr int kSecondItem = 32;    // what a second item costs a block, in units
 constexpr int kJoin = 32;          // blocks of an item joined by one; more are joined in two levels
 constexpr int kAtMaxBlocks = kJoin * kJoin;  // blocks of a grid, at most
 
@@ -453,13 +452,13 @@ struct Geo {
 template <int HD, typename TIO, bool E4M3, int NT>
 struct AtShape {
   static constexpr int kRows = 8 * NT;
-  // Resident warps per SM are what registers allow.  With one tile of rows as small
-  // blocks, which leave fewer items cut and overlap one's prologue with another's
-  // loop (27 us against 34 in blocks of 12 warps, 32 ragged sequences); with more
-  // rows in one block, whose join has half as many parts and twice the threads.
-  static constexpr int kWarps = NT <= 2 ? 4 : 8;
+  // Small blocks leave fewer items cut and overlap one's prologue with another's loop:
+  // 27 us against 34 in one block of 12 warps per SM for 32 ragged sequences, 27.8
+  // against 29.4 in one of 8 warps with groups of 32 rows for 8 blocks of 7 rows.  As many are
+  // resident as registers allow.
+  static constexpr int kWarps = 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kBlocks = NT == 1 || (NT == 2 && (E4M3 || HD == 64)) ? 3 : NT == 2 ? 2 : 1;
+  static constexpr int kBlocks = NT == 1 || E4M3 || HD == 64 ? 3 : 2;
   static constexpr int NQ = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int NP = E4M3 ? 2 : sizeof(TIO) == 4 ? 3 : 2;
   static constexpr int kQBytes = Geo<HD, E4M3>::KS * NQ * NT * 32 * 8;      // fragments of Q^T
@@ -481,7 +480,7 @@ struct AttnArgs {
   PagedAttn a;
   int G, R, n_rg;            // query heads of a KV head, rows of a KV head, row groups
   int vec;                   // rows of q start on 16-byte boundaries
-  int few;                   // up to 32 sequences of up to 8 row groups each, units below 2^31
+  int few;                   // up to 32 sequences of up to 8 row groups each, units below 2^30
   Div by_page, by_G;
   int cap;                   // positions of a page table's row
   float qscale;              // scale * log2(e)
@@ -588,13 +587,20 @@ __device__ __forceinline__ int units_of(int len) { return len < 0 ? 0 : max(1, (
 // Weight of an item of n units when parts hold up to `size`.
 __device__ __forceinline__ int weight_of(int n, int size) { return size == 1 ? n : (n + size - 1) / size; }
 
-// The size of the parts.  Long shares (kLongShare units a block): 1, the line of
-// units is cut into equal shares, an item wherever one ends.  Short ones: a second
-// item in a block costs more than uneven parts do (8 us of a block's 25 for 32
-// sequences of 512 to 2048), so each item is cut into equal parts, one a block, of a
-// size for which the blocks suffice: parts <= units / size + items <= blocks.
-__device__ __forceinline__ int part_size(int units, int items, int grid) {
-  return units >= grid * kLongShare || items >= grid ? 1 : max(kMinUnits, (units + grid - items - 1) / (grid - items));
+// The size of the parts.  1: the line of units is cut into equal shares, an item
+// wherever one ends, so that many blocks work on two items.  Else each item is cut
+// into equal parts, one a block, of the smallest size for which the blocks suffice
+// (parts <= units / size + items <= blocks): no block pays for a second prologue, merge
+// and join, but the longest part (`longest`: the longest item) sets the time.  Parts
+// are taken while that is at most 5/4 of a share and a second item.  Measured, parts
+// against shares: 32 sequences of 512 to 2048 21.8 and 25.7 us; 8 x 4096 34.2 and 37.7;
+// 4 x 131072 330 and 348; 24 of 3000 to 12000 (192 items) 94 and 68.
+template <typename I>
+__device__ __forceinline__ int part_size(I units, I items, int longest, int grid) {
+  if (items >= grid) return 1;
+  const I size = max(static_cast<I>(kMinUnits), (units + grid - items - 1) / (grid - items));
+  const I share = units / grid;
+  return min(size, static_cast<I>(longest)) <= share + share / 4 + kSecondItem && size < (1 << 26) ? static_cast<int>(size) : 1;
 }
 
 // A block's place: weights [u0, u1) of the line, of which sequence b's first is `at`.
@@ -617,10 +623,15 @@ template <int THREADS>
 __device__ __noinline__ Place place_of_many(const AttnArgs &p, int rows, long long *s_scan) {
   constexpr int kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.a.B;
+  int longest = 0;
   auto seq_weight = [&](int b, int size) {
     long long n = 0;
 #pragma unroll 1
-    for (int rg = 0; rg < p.n_rg; ++rg) n += weight_of(units_of(group_len(p, rows, b, rg)), size);
+    for (int rg = 0; rg < p.n_rg; ++rg) {
+      const int units = units_of(group_len(p, rows, b, rg));
+      longest = max(longest, units);
+      n += weight_of(units, size);
+    }
     return n * p.a.kv.n_kv_heads;
   };
   Place w{};
@@ -631,8 +642,12 @@ __device__ __noinline__ Place place_of_many(const AttnArgs &p, int rows, long lo
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     if (pass == 1) {
-      const long long items = static_cast<long long>(B) * p.n_rg * p.a.kv.n_kv_heads, grid = gridDim.x;
-      if (items < grid && line < grid * kLongShare) w.size = part_size(static_cast<int>(line), static_cast<int>(items), gridDim.x);
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      __syncthreads();
+      if (lane == 0) s_scan[warp] = longest;
+      __syncthreads();
+      for (int k = 0; k < kWarps; ++k) longest = max(longest, static_cast<int>(s_scan[k]));
+      w.size = part_size(line, static_cast<long long>(B) * p.n_rg * p.a.kv.n_kv_heads, longest, gridDim.x);
       if (w.size == 1) continue;
     }
     if (pass == 2) {
@@ -679,18 +694,24 @@ __device__ __noinline__ Place place_of_many(const AttnArgs &p, int rows, long lo
 // Up to 32 sequences of a few row groups each: every warp counts for itself.
 __device__ __forceinline__ Place place_of_few(const AttnArgs &p, int rows) {
   const int lane = threadIdx.x & 31, hkv = p.a.kv.n_kv_heads, grid = gridDim.x;
+  int longest = 0;
   auto seq_weight = [&](int size) {
     int n = 0;
     if (lane < p.a.B) {
 #pragma unroll 1
-      for (int rg = 0; rg < p.n_rg; ++rg) n += weight_of(units_of(group_len(p, rows, lane, rg)), size);
+      for (int rg = 0; rg < p.n_rg; ++rg) {
+        const int units = units_of(group_len(p, rows, lane, rg));
+        longest = max(longest, units);
+        n += weight_of(units, size);
+      }
     }
     return n * hkv;
   };
   int n = seq_weight(1);
   int line = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
   Place w{};
-  w.size = part_size(line, p.a.B * p.n_rg * hkv, grid);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  w.size = part_size(line, p.a.B * p.n_rg * hkv, longest, grid);
   if (w.size > 1) n = seq_weight(w.size);
   int incl = n;
 #pragma unroll
@@ -767,8 +788,10 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       }
     }
     const int w0 = static_cast<int>(u - at), w1 = static_cast<int>(min(place.u1 - at, static_cast<long long>(weight)));
-    // units [seg0, seg1) of the item; parts of equal size (products below 2^31: short lines only)
-    const int seg0 = place.size == 1 ? w0 : w0 * cost / weight, seg1 = place.size == 1 ? w1 : w1 * cost / weight;
+    // units [seg0, seg1) of the item; parts of equal size
+    const bool cut_even = place.size > 1;
+    const int seg0 = cut_even ? static_cast<int>(static_cast<long long>(w0) * cost / weight) : w0;
+    const int seg1 = cut_even ? static_cast<int>(static_cast<long long>(w1) * cost / weight) : w1;
     const bool whole = seg0 == 0 && seg1 == cost;
     const int pos = a.positions[b], n_rows = seq_rows(a, b), r0 = rg * kRows;
 
@@ -1382,7 +1405,7 @@ static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStr
   const int blocks = std::min(n_sm * S::kBlocks, kAtMaxBlocks);
   p.n_rg = (p.R + S::kRows - 1) / S::kRows;
   p.few = p.a.B <= 32 && p.n_rg <= 8 &&
-          static_cast<long long>(p.a.B) * p.n_rg * p.a.kv.n_kv_heads * (p.cap / kUnit + 1) < (1ll << 31);
+          static_cast<long long>(p.a.B) * p.n_rg * p.a.kv.n_kv_heads * (p.cap / kUnit + 1) < (1ll << 30);
   p.count = static_cast<uint32_t *>(workspace);
   p.part = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + kCountBytes);
   p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD / 4);
