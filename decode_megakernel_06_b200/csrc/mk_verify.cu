@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
   cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ __align__(16) unsigned char dyn[];
   RowsShared &sh = *reinterpret_cast<RowsShared *>(dyn);
-  float *queue = reinterpret_cast<float *>(dyn + sizeof(RowsShared));  // [kQueue][kVThreads], then [kCache]
-  float *cache = queue + kQueue * kVThreads;
+  float *queue = reinterpret_cast<float *>(dyn + sizeof(RowsShared));  // [kQueue + 1][kVThreads], then [kCache]
+  float *cache = queue + (kQueue + 1) * kVThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = cluster.block_rank(), size = cluster.num_blocks();
   const int row = blockIdx.x / size;
@@ -231,8 +231,17 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
 
   // ---- the largest logit ---------------------------------------------------------------
   float mx = -INFINITY;
-  if (a.cached) {
-    each<4>(src, n, a.vec4, tid, [&](float x, int i) {
+  if (a.cached && a.vec4) {
+    const float4 *s4 = reinterpret_cast<const float4 *>(src);
+    float4 *c4 = reinterpret_cast<float4 *>(cache);
+#pragma unroll 8
+    for (int i = tid; i < n / 4; i += kVThreads) {
+      const float4 x = s4[i];
+      c4[i] = x;
+      mx = fmaxf(mx, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+    }
+  } else if (a.cached) {
+    each<4>(src, n, 0, tid, [&](float x, int i) {
       if (i < n) cache[i] = x;
       mx = fmaxf(mx, x);
     });
@@ -359,11 +368,12 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
 #pragma unroll 1
     for (int tries = 0; tries < kBins; ++tries) {
       queued = 0;
-      each<2>(src, n, a.vec4, tid, [&](float x, int i) {
-        if (i < n && (fine_of(x) >> kFine) <= bin) {
-          if (queued < kQueue) queue[queued * kVThreads + tid] = x;
-          ++queued;
-        }
+      // fine_of(x) >> kFine <= bin, as the sum with 2^23 rounds; behind the end at is infinite
+      const float lim = bin < kBins - 1 ? static_cast<float>((bin + 1) << kFine) - 0.5f : 3e38f;
+      each<2>(src, n, a.vec4, tid, [&](float x, int) {
+        // written at the queue's end in any case, which a branch would cost more than
+        queue[min(queued, kQueue) * kVThreads + tid] = x;
+        queued += (m - x) * a.bin_scale < lim;
       });
       listed = !__syncthreads_or(queued > kQueue);
       u64 more = 0, in = 0;
@@ -906,7 +916,7 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   r.stats = stats;
   static std::atomic<size_t> set_rows[kVerifyDevices];
   r.cached = !greedy && v.top_p < 1.0f && r.slice <= kCache;
-  const size_t smem_rows = sizeof(RowsShared) + (greedy ? 0 : sizeof(float) * kQueue * kVThreads) +
+  const size_t smem_rows = sizeof(RowsShared) + (greedy ? 0 : sizeof(float) * (kQueue + 1) * kVThreads) +
                            (r.cached ? sizeof(float) * kCache : 0);
   e = allow_smem(verify_rows, smem_rows, set_rows);
   if (e == cudaSuccess) e = launch(verify_rows, rows, cr, kVThreads, smem_rows, st, r);
