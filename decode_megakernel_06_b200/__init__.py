@@ -11,6 +11,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -304,6 +305,11 @@ def _need(t, dtype, min_numel: int, name: str, device=None, dims: Optional[int] 
         raise ValueError(f"{name}: on {t.device}, expected " + (str(device) if device is not None else "a CUDA device"))
 
 
+def _fits(t, dtype, min_numel: int, index: int) -> bool:
+    """Whether _need would accept t, on CUDA device ``index``."""
+    return t is not None and t.dtype is dtype and t.get_device() == index and t.numel() >= min_numel and t.is_contiguous()
+
+
 def sample_top_p(logits, temperature: float, top_p: float, uniforms, out_tokens, stream=None) -> int:
     """Torch-tensor form of mk_sample_top_p: logits fp32 [rows, vocab], uniforms
     fp64 [rows] (or None when temperature <= 0), out_tokens int32 [rows], all
@@ -356,13 +362,25 @@ def _call_on(index: int, call, *args) -> int:
 def _raw_stream(index: int, stream) -> int:
     """The CUDA stream of a call on device ``index``: the given one, which has to
     be that device's, or its current one."""
-    import torch
-
+    global _current_raw_stream
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        if _current_raw_stream is None:
+            import torch
+
+            _current_raw_stream = torch._C._cuda_getCurrentRawStream
+        return _current_raw_stream(index)
     if stream.device.index != index:
         raise ValueError(f"stream: on {stream.device}, expected cuda:{index}")
     return stream.cuda_stream
+
+
+_current_raw_stream = None
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(seq: int, token: int, head: int) -> mk_strides:
+    """The struct of an operand's strides (passed by value)."""
+    return mk_strides(seq, token, head)
 
 
 class PagedKV:
@@ -399,6 +417,8 @@ class PagedKV:
         self._index, self._batch, self._heads, self._hd = self.device.index, page_table.shape[0], heads, hd
         self._kinds = {torch.float32: MK_F32, torch.bfloat16: MK_BF16}
         self._int, self._byte = torch.int32, torch.uint8
+        self._lib, self._ref = lib(), ctypes.byref(self.desc)
+        self._current_device = torch.cuda.current_device
 
     def _rows(self, t, name: str, heads: Optional[int]):
         """Checks a [B, T, heads, head_dim] operand (fp32 or bf16, any strides but a
@@ -416,13 +436,19 @@ class PagedKV:
                              f"{'heads' if heads is None else heads}, {self._hd}]")
         return shape, st, kind
 
+    def _call(self, call, *args) -> int:
+        """call(cache, *args) with the cache's device current."""
+        if self._current_device() == self._index:
+            return call(self._ref, *args)
+        return _call_on(self._index, call, self._ref, *args)
+
     def _pair(self, x, y, names: Sequence[str]):
         """Two such operands of one shape and type: (B, T), the type and both strides."""
         shape, st, kind = self._rows(x, names[0], self._heads)
         other, st2, kind2 = self._rows(y, names[1], self._heads)
         if other != shape or kind2 != kind:
             raise ValueError(f"{names[1]}: {tuple(other)} {y.dtype}, expected {tuple(shape)} {x.dtype}")
-        return shape[0], shape[1], kind, mk_strides(st[0], st[1], st[2]), mk_strides(st2[0], st2[1], st2[2])
+        return shape[0], shape[1], kind, st, st2
 
     def _ints(self, t, name: str) -> int:
         """An int32 operand with an entry per sequence; its pointer."""
@@ -450,8 +476,8 @@ class PagedKV:
         pos = self._ints(positions, "positions")
         cnt = None if counts is None else self._ints(counts, "counts")
         table, n = self._rope(rope)
-        return _call_on(self._index, mk_kv_append, self.desc, k.data_ptr(), ks, v.data_ptr(), vs, kind, pos, cnt, B,
-                        T, table, n, _raw_stream(self._index, stream))
+        return self._call(self._lib.mk_kv_append, k.data_ptr(), _strides(*ks[:3]), v.data_ptr(), _strides(*vs[:3]), kind,
+                          pos, cnt, B, T, table, n, _raw_stream(self._index, stream))
 
     def gather(self, starts, out_k, out_v, counts=None, stream=None) -> int:
         """mk_kv_gather: positions starts[b] + t into out_k, out_v
@@ -459,12 +485,12 @@ class PagedKV:
         [B, heads, capacity, head_dim] transposed)."""
         B, T, kind, ks, vs = self._pair(out_k, out_v, ("out_k", "out_v"))
         for name, s in (("out_k", ks), ("out_v", vs)):
-            if (s.seq == 0 and B > 1) or (s.token == 0 and T > 1) or (s.head == 0 and self._heads > 1):
+            if 0 in s and ((s[0] == 0 and B > 1) or (s[1] == 0 and T > 1) or (s[2] == 0 and self._heads > 1)):
                 raise ValueError(f"{name}: written rows must not share memory")
         pos = self._ints(starts, "starts")
         cnt = None if counts is None else self._ints(counts, "counts")
-        return _call_on(self._index, mk_kv_gather, self.desc, pos, cnt, B, T, out_k.data_ptr(), ks, out_v.data_ptr(),
-                        vs, kind, _raw_stream(self._index, stream))
+        return self._call(self._lib.mk_kv_gather, pos, cnt, B, T, out_k.data_ptr(), _strides(*ks[:3]), out_v.data_ptr(),
+                          _strides(*vs[:3]), kind, _raw_stream(self._index, stream))
 
     def attention(self, q, positions, out, workspace, counts=None, scale: Optional[float] = None, rope=None,
                   stream=None) -> int:
@@ -482,9 +508,9 @@ class PagedKV:
             _need(workspace, self._byte, 1, "workspace", self.device)
         if scale is None:
             scale = self._hd ** -0.5
-        return _call_on(self._index, mk_paged_attention, self.desc, q.data_ptr(), mk_strides(st[0], st[1], st[2]),
-                        kind, shape[2], pos, cnt, shape[0], shape[1], scale, table, n, out.data_ptr(),
-                        workspace.data_ptr(), workspace.numel(), _raw_stream(self._index, stream))
+        return self._call(self._lib.mk_paged_attention, q.data_ptr(), _strides(*st[:3]), kind, shape[2], pos, cnt,
+                          shape[0], shape[1], scale, table, n, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                          _raw_stream(self._index, stream))
 
 
 def paged_attention_workspace(device):
@@ -518,22 +544,23 @@ def verify_sample(logits, tokens, temperature: float, top_p: float, uniforms, ou
     device (ValueError otherwise).  Returns the launch status code."""
     import torch
 
-    _need(logits, torch.float32, 1, "logits", dims=3)
-    dev = logits.device
+    if logits.dim() != 3 or not _fits(logits, torch.float32, 1, logits.get_device()) or not logits.is_cuda:
+        _need(logits, torch.float32, 1, "logits", dims=3)
+    index = logits.get_device()
     B, T, vocab = logits.shape
-    _need(tokens, torch.int32, B * T, "tokens", dev)
-    if draft_logits is not None:
-        _need(draft_logits, torch.float32, 0, "draft_logits", dev, dims=3)
-        if tuple(draft_logits.shape) != (B, T - 1, vocab):
-            raise ValueError(f"draft_logits: shape {tuple(draft_logits.shape)}, expected {(B, T - 1, vocab)}")
-    if uniforms is not None:
-        _need(uniforms, torch.float64, B * T, "uniforms", dev)
-    _need(out_tokens, torch.int32, B * T, "out_tokens", dev)
-    _need(out_accepted, torch.int32, B, "out_accepted", dev)
-    _need(workspace, torch.uint8, 1, "workspace", dev)
-    return _call_on(dev.index, mk_verify_sample, logits.data_ptr(), _ptr(draft_logits) if T > 1 else None,
-                    tokens.data_ptr(), B, T, vocab, temperature, top_p, _ptr(uniforms), out_tokens.data_ptr(),
-                    out_accepted.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index, stream))
+    rows = B * T
+    for t, dtype, n, name in ((tokens, torch.int32, rows, "tokens"), (uniforms, torch.float64, rows, "uniforms"),
+                              (out_tokens, torch.int32, rows, "out_tokens"),
+                              (out_accepted, torch.int32, B, "out_accepted"), (workspace, torch.uint8, 1, "workspace"),
+                              (draft_logits, torch.float32, 0, "draft_logits")):
+        if not _fits(t, dtype, n, index) and (t is not None or name not in ("uniforms", "draft_logits")):
+            _need(t, dtype, n, name, logits.device)
+    if draft_logits is not None and draft_logits.shape != (B, T - 1, vocab):
+        raise ValueError(f"draft_logits: shape {tuple(draft_logits.shape)}, expected {(B, T - 1, vocab)}")
+    args = (logits.data_ptr(), _ptr(draft_logits) if T > 1 else None, tokens.data_ptr(), B, T, vocab, temperature, top_p,
+            _ptr(uniforms), out_tokens.data_ptr(), out_accepted.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _raw_stream(index, stream))
+    return _call_on(index, lib().mk_verify_sample, *args)
 
 
 def hbm_read_probe(buf, form: int = 0, reps: int = 5, stream=None) -> float:
