@@ -442,8 +442,10 @@ struct Lazy {
 constexpr float kLeastScale = -80.0f;  // log2 of scales below it counts as this: the sums of weights stay finite
 constexpr int kMinUnits = 8;       // units per block, at least
 constexpr int kSecondItem = 32;    // what a second item costs a block, in units
-constexpr int kJoin = 32;          // blocks of an item joined by one; more are joined in two levels
-constexpr int kAtMaxBlocks = kJoin * kJoin;  // blocks of a grid, at most
+constexpr int kJoinBits = 3;       // parts of an item that one block joins, all their loads in flight; more are
+constexpr int kJoin = 1 << kJoinBits;  // joined in levels (one cache of 8192: 23.5 us by 32 at a time, 20.7 by 16, 18.5 by 8)
+constexpr int kLevels = 3;
+constexpr int kAtMaxBlocks = kJoin * kJoin * kJoin;  // blocks of a grid, at most
 
 template <int HD, bool E4M3>
 struct Geo {
@@ -498,7 +500,7 @@ struct AttnArgs {
   float qscale;              // scale * log2(e)
   float4 *part;              // [2 * blocks][kRows][HD / 4] sums
   float2 *part_ml;           // [2 * blocks][kRows] (reference, sum of weights)
-  uint32_t *count;           // [kAtMaxBlocks] per item, then [2 * kAtMaxBlocks] per group of a join's first level
+  uint32_t *count;           // [kLevels][2 * blocks]: arrivals at a group's first part
 };
 
 __device__ __forceinline__ uint4 ld_cache(const uint4 *p) {
@@ -977,12 +979,10 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       const int after = row_at(unit + 2 * kAtWarps);
       prefetch(after);
       const int p0 = unit * kUnit;
-      // S^T = K Q^T, one sum per piece of q while there are few tiles: the chains of
-      // dependent products are shorter
-      constexpr int kSums = NT <= 2 ? NQ : 1;
-      float sp[kSums][NT][4];
+      // S^T = K Q^T, one sum per piece of q: shorter chains of dependent products
+      float sp[NQ][NT][4];
 #pragma unroll
-      for (int i = 0; i < kSums; ++i)
+      for (int i = 0; i < NQ; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1006,7 +1006,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint2 q = qfrag[((k * NT + n) * NQ + i) * 32 + lane];
-            mma<E4M3>(sp[i % kSums][n], a0, a1, a2, a3, q.x, q.y);
+            mma<E4M3>(sp[i][n], a0, a1, a2, a3, q.x, q.y);
           }
       }
       float s[NT][4];
@@ -1014,9 +1014,9 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[n][j] = sp[kSums - 1][n][j];
+          s[n][j] = sp[NQ - 1][n][j];
 #pragma unroll
-          for (int i = kSums - 2; i >= 0; --i) s[n][j] += sp[i][n][j];
+          for (int i = NQ - 2; i >= 0; --i) s[n][j] += sp[i][n][j];
         }
       float ks_[2] = {1.f, 1.f}, vs_[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
       if constexpr (E4M3) {
@@ -1260,19 +1260,16 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll 1
       for (int i = tid; i < kPieces; i += kAtThreads) __stcg(p.part + static_cast<long long>(slot_of(me)) * kPieces + i, summed(i));
       if (tid < kRows) __stcg(p.part_ml + slot_of(me) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
-      // The parts of up to kJoin blocks b0, b0 + step, .. are joined by the last of them
-      // to arrive at their counter: into the output, or, of an item in more blocks,
-      // first in groups, back into the part of each group's first block.
+      // A tree of joins: the last of kJoin parts to arrive at their group's counter joins
+      // them, in their order, into the output, or into the group's first part, which is one
+      // of the next level's.
       const int n_parts = last - first + 1;
-      int b0 = first, parts = n_parts, step = 1;
-      uint32_t *counter = p.count + first;
-      if (n_parts > kJoin) {
-        b0 = first + (me - first) / kJoin * kJoin;
-        parts = min(last - b0 + 1, kJoin);
-        counter = p.count + kAtMaxBlocks + slot_of(b0);
-      }
 #pragma unroll 1
-      for (;;) {
+      for (int level = 0, bits = 0;; ++level, bits += kJoinBits) {
+        const int step = 1 << bits, span = step << kJoinBits, b0 = first + ((me - first) & -span);
+        const int parts = (min(last - b0 + 1, span) + step - 1) >> bits;
+        uint32_t *counter = p.count + level * 2 * gridDim.x + slot_of(b0);
+        const bool final = span >= n_parts;
         __syncthreads();  // the block's part is written; the release below makes it seen
         if (tid == 0) {
           uint32_t old;
@@ -1282,60 +1279,63 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         }
         __syncthreads();
         if (!s_last) break;
-        const bool final = n_parts <= kJoin || step > 1;
+        // two pieces at a time
+        static_assert(kPieces % (2 * kAtThreads) == 0 || kPieces == kAtThreads, "pieces per thread");
+        constexpr int kAtOnce = kPieces == kAtThreads ? 1 : 2;
 #pragma unroll 1
-        for (int i = tid; i < kPieces; i += kAtThreads) {
-          const int r = i / kRowPieces;
-          float M = -INFINITY, L = 0.f;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-          for (int k0 = 0; k0 < parts; k0 += 8) {
-            float4 y[8];
-            float2 ml[8];
+        for (int i0 = tid; i0 < kPieces; i0 += kAtOnce * kAtThreads) {
+          float M[kAtOnce], L[kAtOnce];
+          float4 x[kAtOnce];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // behind the last part: the last again, without weight
-              const int slot = slot_of(b0 + min(k0 + k, parts - 1) * step);
-              ml[k] = __ldcg(p.part_ml + slot * kRows + r);
-              y[k] = __ldcg(p.part + static_cast<long long>(slot) * kPieces + i);
+          for (int e = 0; e < kAtOnce; ++e) {
+            M[e] = -INFINITY;
+            L[e] = 0.f;
+            x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          float4 y[kAtOnce][kJoin];
+          float2 ml[kAtOnce][kJoin];
+#pragma unroll
+          for (int k = 0; k < kJoin; ++k) {  // behind the last part: the last again, without weight
+            const int slot = slot_of(b0 + (min(k, parts - 1) << bits));
+            const float4 *src = p.part + static_cast<long long>(slot) * kPieces + i0;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+              ml[e][k] = __ldcg(p.part_ml + slot * kRows + (i0 + e * kAtThreads) / kRowPieces);
+              y[e][k] = __ldcg(src + e * kAtThreads);
             }
-            float to = M;
+          }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to = fmaxf(to, ml[k].x);
-            const float old = to == -INFINITY ? 1.f : ex2(M - to);
-            M = to;
-            L *= old;
-            x.x *= old;
-            x.y *= old;
-            x.z *= old;
-            x.w *= old;
+          for (int e = 0; e < kAtOnce; ++e) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k0 + k < parts) {
-                const float by = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - M);
-                L = fmaf(ml[k].y, by, L);
-                x.x = fmaf(y[k].x, by, x.x);
-                x.y = fmaf(y[k].y, by, x.y);
-                x.z = fmaf(y[k].z, by, x.z);
-                x.w = fmaf(y[k].w, by, x.w);
+            for (int k = 0; k < kJoin; ++k) M[e] = fmaxf(M[e], ml[e][k].x);
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k)
+              if (k < parts) {
+                const float by = ml[e][k].x == -INFINITY ? 1.f : ex2(ml[e][k].x - M[e]);
+                L[e] = fmaf(ml[e][k].y, by, L[e]);
+                x[e].x = fmaf(y[e][k].x, by, x[e].x);
+                x[e].y = fmaf(y[e][k].y, by, x[e].y);
+                x[e].z = fmaf(y[e][k].z, by, x[e].z);
+                x[e].w = fmaf(y[e][k].w, by, x[e].w);
               }
           }
-          if (final) {
-            finish(i, x, L);
-          } else {
-            __stcg(p.part + static_cast<long long>(slot_of(b0)) * kPieces + i, x);  // read by this thread alone
-            if (i % kRowPieces == 0) {
-              s_M[r] = M;
-              s_L[r] = L;
+#pragma unroll
+          for (int e = 0; e < kAtOnce; ++e) {
+            const int i = i0 + e * kAtThreads, r = i / kRowPieces;
+            if (final) {
+              finish(i, x[e], L[e]);
+            } else {
+              __stcg(p.part + static_cast<long long>(slot_of(b0)) * kPieces + i, x[e]);  // read by this thread alone
+              if (i % kRowPieces == 0) {
+                s_M[r] = M[e];
+                s_L[r] = L[e];
+              }
             }
           }
         }
         if (final) break;
         __syncthreads();  // every thread has read b0's reference
         if (tid < kRows) __stcg(p.part_ml + slot_of(b0) * kRows + tid, make_float2(s_M[tid], s_L[tid]));
-        b0 = first;
-        step = kJoin;
-        parts = (n_parts + kJoin - 1) / kJoin;
-        counter = p.count + first;
       }
     }
     u = at + w1;
@@ -1401,9 +1401,9 @@ cudaError_t launch_kv_gather(const KvGather &args, int out_dtype, cudaStream_t s
               : launch(kv_gather<128, __nv_bfloat16, false>, grid, block, 0, st, a);
 }
 
-// Workspace: counters (one per block, two per block for the first level of a join), then
-// the parts of at most two items per block, laid out for the most rows.
-constexpr size_t kCountBytes = sizeof(uint32_t) * 3 * kAtMaxBlocks;
+// Workspace: counters (of at most two items per block, for each level of a join), then
+// the parts, laid out for the most rows.
+constexpr size_t kCountBytes = sizeof(uint32_t) * kLevels * 2 * kAtMaxBlocks;
 
 size_t paged_attention_workspace(int n_sm) {
   // two parts of 16 rows in 3 blocks per SM: more than of 8 rows
