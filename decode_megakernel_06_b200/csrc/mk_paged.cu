@@ -812,17 +812,20 @@ paged_attn(const __grid_constant__ AttnArgs p) {
     // ---- loads of a unit, a whole one ahead of its products ------------------------------
     const int32_t *table = a.kv.page_table + static_cast<long long>(b) * a.kv.max_pages;
     const long long all_see = static_cast<long long>(pos) + p.by_G.of(r0);  // last position that every row sees
-    // pool row of position q, and of position 16 unit + lane % 16; -1: none
-    auto row_of = [&](int q) {
-      const int e = p.by_page.of(q);
-      const int page = table[e];
-      if (page < 0 || page >= a.kv.n_pages) return -1;
-      return (page * a.kv.n_kv_heads + h) * a.kv.page_size + (q - e * a.kv.page_size);
+    // A position's page (-1: none), and its pool row (-1: none) once that is known; the
+    // position of a lane is 16 unit + lane % 16.  Selects, no branches: several pages'
+    // numbers are then on their way at once.
+    auto page_of = [&](int q, bool in) { return in ? table[p.by_page.of(q)] : -1; };
+    auto row_of = [&](int q, int page) {
+      const unsigned in_page = q - p.by_page.of(q) * a.kv.page_size;
+      const unsigned row = (static_cast<unsigned>(page) * a.kv.n_kv_heads + h) * a.kv.page_size + in_page;
+      return static_cast<unsigned>(page) < static_cast<unsigned>(a.kv.n_pages) ? static_cast<int>(row) : -1;
     };
-    auto row_at = [&](int unit) {
+    auto page_at = [&](int unit) {
       const int q = unit * kUnit + (lane & 15);
-      return unit >= seg1 || q >= len ? -1 : row_of(q);
+      return page_of(q, unit < seg1 && q < len);
     };
+    auto row_at = [&](int unit, int page) { return row_of(unit * kUnit + (lane & 15), page); };
     uint32_t kw[2][KW], vw[4][VW];
     float ksc = 0.f, vsc = 0.f;  // scales of position lane % 16
     auto load_k = [&](int row) {
@@ -865,7 +868,8 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
       for (int i = 0; i < HD * X::kBytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
     };
-    int row = row_at(seg0 + warp), next = row_at(seg0 + warp + kAtWarps);
+    const int page0 = page_at(seg0 + warp), page1 = page_at(seg0 + warp + kAtWarps);
+    int row, next;
 
     // ---- Q: rotated, in pieces, in the layout of the product's B operand -----------------
     {
@@ -894,7 +898,9 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           }
         }
       }
-      load_k(row);  // the first unit's loads wait for its page's number; the rows' are on their way
+      row = row_at(seg0 + warp, page0);  // the queries are on their way
+      next = row_at(seg0 + warp + kAtWarps, page1);
+      load_k(row);
       load_v(row);
       prefetch(next);
       float x[kQuads][4], y[kQuads][4];
@@ -976,7 +982,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         for (int j = 0; j < 4; ++j) acc[t][n][j] = 0.f;
     }
     for (int unit = seg0 + warp; unit < seg1; unit += kAtWarps) {
-      const int after = row_at(unit + 2 * kAtWarps);
+      const int after = row_at(unit + 2 * kAtWarps, page_at(unit + 2 * kAtWarps));
       prefetch(after);
       const int p0 = unit * kUnit;
       // S^T = K Q^T, one sum per piece of q: shorter chains of dependent products
@@ -1217,7 +1223,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       const int p1 = static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(seg1) * kUnit));
 #pragma unroll 1
       for (int q = max(static_cast<int>(max(all_see + 1, 0ll)), seg0 * kUnit); q < p1; ++q) {
-        const int r = row_of(q);
+        const int r = row_of(q, page_of(q, true));
         if (r < 0) continue;
 #pragma unroll 1
         for (int i = tid; i < kRows * HD; i += kAtThreads) {
