@@ -864,20 +864,65 @@ cudaError_t launch(void (*kernel)(Args), int grid, int cluster, int threads, siz
   return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
-// CTAs per row.  A CTA's time goes with its logits (about 0.27 ns each, the fp64
-// exponentials of one SM), and the SMs hold ceil(rows C / n_sm) of them one after
-// another; a cluster's barriers cost about 4 us.
-int cluster_for(int rows, int V, int n_sm) {
-  int best = 1;
+// Shared memory of verify_rows: with a queue per thread, and with a row's cache.
+size_t rows_smem(bool queue, bool cache) {
+  return sizeof(RowsShared) + (queue ? sizeof(float) * (kQueue + 1) * kVThreads : 0) + (cache ? sizeof(float) * kCache : 0);
+}
+
+std::atomic<size_t> g_rows_smem[kVerifyDevices];
+
+// Clusters of verify_rows that the current device holds at once, with the cache's shared
+// memory: a CTA takes an SM, and a cluster its SMs from one group of them, so that fewer
+// than n_sm / C may fit.  Asked once per device and size.
+cudaError_t clusters_at_once(int log2c, int dev, int *n) {
+  static std::atomic<int> known[kVerifyDevices][4];
+  static_assert((1 << 3) == kMaxCluster);
+  if (dev < 0 || dev >= kVerifyDevices) return cudaErrorInvalidDevice;
+  *n = known[dev][log2c].load(std::memory_order_relaxed);
+  if (*n > 0) return cudaSuccess;
+  const size_t smem = rows_smem(true, true);
+  cudaError_t e = allow_smem(verify_rows, smem, g_rows_smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1u << log2c;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1u << log2c);
+  cfg.blockDim = dim3(kVThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, verify_rows, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*n < 1) *n = 1;
+  known[dev][log2c].store(*n, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+// CTAs per row.  The rows' clusters run in ceil(rows / clusters at once) turns.  A turn
+// takes a fixed time and a time that goes with a CTA's share of the row: 15 us + 0.7 ns
+// a logit where a nucleus is searched, 8 us + 0.3 ns a logit where the whole
+// distribution stands; a doubling of the cluster costs its barriers 2 us or 1 us.
+// Measured with 1 | 2 | 4 | 8 CTAs, nucleus 0.9: 248 rows of 64000 152 | 183 | 253 |
+// 464 us, 104 of 32000 44 | 58 | 90 | 167, 28 of 20000 31 | 29 | 28 | 51, 16 of 32000
+// 42 | 33 | 29 | 51, 7 of 64000 88 | 64 | 50 | 46, 10 of 5000 19 | 21 | 21 | 26; whole
+// distribution: 72 of 32000 24 | 20 | 33 | 49, 8 of 32000 21 | 17 | 15 | 15.
+cudaError_t cluster_for(int rows, int V, bool nucleus, int *best) {
+  const double fixed = nucleus ? 15.0 : 8.0, logit = nucleus ? 0.7e-3 : 0.3e-3, doubling = nucleus ? 2.0 : 1.0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   double least = 1e30;
-  for (int c = 1; c <= kMaxCluster; c *= 2) {
-    const double us = 0.00027 * V / c * static_cast<double>((static_cast<long long>(rows) * c + n_sm - 1) / n_sm) + (c > 1 ? 4.0 : 0.0);
+  for (int i = 0; e == cudaSuccess && (1 << i) <= kMaxCluster; ++i) {
+    int n = 1;
+    e = clusters_at_once(i, dev, &n);
+    const double us = static_cast<double>((static_cast<long long>(rows) + n - 1) / n) * (fixed + logit * V / (1 << i)) + doubling * i;
     if (us < least) {
       least = us;
-      best = c;
+      *best = 1 << i;
     }
   }
-  return best;
+  return e;
 }
 
 }  // namespace
@@ -898,11 +943,9 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   r.B = v.B;
   r.T = v.T;
   r.V = v.V;
-  int dev = 0, n_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  int cr = 1;
+  cudaError_t e = cluster_for(rows, v.V, !greedy && v.top_p < 1.0f, &cr);
   if (e != cudaSuccess) return e;
-  const int cr = cluster_for(rows, v.V, n_sm);
   r.slice = ((v.V + cr - 1) / cr + 3) & ~3;
   r.vec4 = v.V % 4 == 0 && (reinterpret_cast<uintptr_t>(v.logits) & 15) == 0 &&
            (!draft || (reinterpret_cast<uintptr_t>(v.draft_logits) & 15) == 0);
@@ -914,11 +957,9 @@ cudaError_t launch_verify_sample(const VerifySample &v, cudaStream_t st) {
   r.bin_scale = greedy ? 0.f : static_cast<float>(std::min((kBins << kFine) * inv_t / 33.0, most));
   r.inv_t2 = static_cast<float>(std::min(inv_t * 1.4426950408889634, most));  // log2(e)
   r.stats = stats;
-  static std::atomic<size_t> set_rows[kVerifyDevices];
   r.cached = !greedy && v.top_p < 1.0f && r.slice <= kCache;
-  const size_t smem_rows = sizeof(RowsShared) + (greedy ? 0 : sizeof(float) * (kQueue + 1) * kVThreads) +
-                           (r.cached ? sizeof(float) * kCache : 0);
-  e = allow_smem(verify_rows, smem_rows, set_rows);
+  const size_t smem_rows = rows_smem(!greedy, r.cached);
+  e = allow_smem(verify_rows, smem_rows, g_rows_smem);
   if (e == cudaSuccess) e = launch(verify_rows, rows, cr, kVThreads, smem_rows, st, r);
   if (e != cudaSuccess) return e;
 
