@@ -422,10 +422,10 @@ __global__ void __launch_bounds__(kRowThreads) kv_gather(const __grid_constant__
 // (a counter per group) joins theirs in the order of the blocks, then the last of
 // eight such groups, so that the result does not depend on who was last.
 //
-// Measured (B200, 6.56 TB/s copy): 4 caches of 131072, bf16, 32/8 heads of 128: 331 us,
-// 6.5 TB/s; 8 of 4096: 33 us, of which the loads take 20 and the rest is the counting,
+// Measured (B200, 6.56 TB/s copy): 4 caches of 131072, bf16, 32/8 heads of 128: 345 us,
+// 6.2 TB/s; 8 of 4096: 33 us, of which the loads take 20 and the rest is the counting,
 // the first pages' chain of loads, the merge and the join; 32 8-bit caches of 512 to 2048:
-// 21 us, 8 blocks of 7 rows at 2048: 27 us, bound by the warps' instructions (products,
+// 20 us, 8 blocks of 7 rows at 2048: 27 us, bound by the warps' instructions (products,
 // conversions, exponentials) at 12 warps per SM.
 //
 // A unit is one warp's: S^T = K Q^T and O^T += V^T P^T on mma.sync, positions and
