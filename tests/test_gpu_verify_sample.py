@@ -81,6 +81,16 @@ def test_against_oracle(B, T, V, certain):
     assert checked >= total - max(1, total // 50), (checked, total)
 
 
+# Rows enough to take one CTA each, of slices too long for its cache, and two CTAs each.
+@pytest.mark.parametrize("B,T,V", [(16, 8, 64000), (11, 8, 40001), (4, 8, 32000)])
+def test_many_rows_of_long_vocabularies(B, T, V):
+    checked = 0
+    for i, (temp, top_p) in enumerate([(0.8, 0.9), (1.2, 0.4)]):
+        lg, dr, tok, u = block(B, T, V, 7 * i + V, temperature=temp)
+        checked += compare(lg, dr, tok, temp, top_p, u)
+    assert checked >= 2 * B - 2, checked
+
+
 def test_ties_and_signed_zeros():
     B, T, V = 4, 4, 3000
     lg, dr, tok, u = block(B, T, V, 1)
