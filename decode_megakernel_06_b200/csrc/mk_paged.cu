@@ -127,17 +127,17 @@ struct Four<__nv_bfloat16> {
 // `spread`-th of its KV heads: the place of the token is looked up once, its
 // rotary angles are held in registers, and the next head's rows are in flight while
 // one's are rounded.  Sixteen values a lane: what is done once per row and lane (the
-// largest value, its scale, a reciprocal, addresses) is most of the instructions.  A key row is rotated in fp32; then each value is rounded once:
-// to bf16, or to the e4m3 code of x / scale with scale = max(amax / 448, 2^-126)
-// over the row's finite values (half a step of e4m3, 2^-4 relative; a true quotient
-// keeps x = amax on the largest code).  Every lane of a warp stays in the shuffles;
-// rows without a place are not written.  Each input byte is read once, each cache byte
+// largest value, its scale, a reciprocal, addresses) is most of the instructions.  A key
+// row is rotated in fp32; then each value is rounded once: to bf16, or to the e4m3 code
+// of x / scale with scale = max(amax / 448, 2^-126) over the row's finite values (half a
+// step of e4m3, 2^-4 relative; a true quotient keeps x = amax on the largest code).
+// Every lane of a warp stays in the shuffles; rows without a place are not written.  Each input byte is read once, each cache byte
 // written once: 30.4 us for 135 MB (4.4 TB/s), bound by the instructions of rounding
 // and scaling beside the loads' latency.
 // ---------------------------------------------------------------------------
 constexpr int kHeadsAtOnce = 2;  // heads whose key and value rows a group of a gather loads together
 
-// Eight consecutive values of a row in their own type.
+// Eight values of a row in their own type: two fours.
 template <typename T>
 struct Eight {
   Four<T> lo, hi;
@@ -145,13 +145,13 @@ struct Eight {
     lo.clear();
     hi.clear();
   }
-  __device__ __forceinline__ void load(const T *p, int vec) {
+  __device__ __forceinline__ void load(const T *p, int second, int vec) {  // the last four at p + second; bf16: 4
     if (sizeof(T) == 2 && vec) {  // one 16-byte load
       const uint4 u = *reinterpret_cast<const uint4 *>(p);
       set(u);
     } else {
       lo.load(p, vec);
-      hi.load(p + 4, vec);
+      hi.load(p + second, vec);
     }
   }
   __device__ __forceinline__ void set(const uint4 &u) {
@@ -182,9 +182,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// Rounds a row and writes it at dst (its scale at *scale_at): a lane holds dimensions
-// 8 lane .. 8 lane + 7 in x[0 .. 3] and HD / 2 + 8 lane .. in x[4 .. 7].
-template <int HD, bool E4M3>
+// Rounds a row and writes it at dst (its scale at *scale_at): a lane holds eight
+// dimensions of the lower half in x[0 .. 3], the second four kSecond behind the first,
+// and those HD / 2 above them in x[4 .. 7].
+template <int HD, bool E4M3, int kSecond>
 __device__ __forceinline__ void put_row(char *dst, float *scale_at, bool on, float2 (&x)[8], int lane) {
   constexpr int kLanes = HD / 16;
   if constexpr (E4M3) {
@@ -230,8 +231,13 @@ __device__ __forceinline__ void put_row(char *dst, float *scale_at, bool on, flo
       w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q[2 * i], __NV_SATFINITE, __NV_E4M3)) |
              static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q[2 * i + 1], __NV_SATFINITE, __NV_E4M3)) << 16;
     if (on) {
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2 *>(dst + HD / 2) = make_uint2(w[2], w[3]);
+      if constexpr (kSecond == 4) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(dst + HD / 2) = make_uint2(w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(dst + i / 2 * (HD / 2) + i % 2 * kSecond) = w[i];
+      }
       if (lane == 0) *scale_at = scale;
     }
   } else if (on) {
@@ -241,8 +247,14 @@ __device__ __forceinline__ void put_row(char *dst, float *scale_at, bool on, flo
       const __nv_bfloat162 v = __floats2bfloat162_rn(x[i].x, x[i].y);
       w[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(dst + HD) = make_uint4(w[4], w[5], w[6], w[7]);
+    if constexpr (kSecond == 4) {
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(dst + HD) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2 *>(dst + i / 2 * HD + i % 2 * (2 * kSecond)) = make_uint2(w[2 * i], w[2 * i + 1]);
+    }
   }
 }
 
@@ -253,6 +265,12 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_cons
   pdl_wait();
   pdl_launch();
   constexpr int kLanes = HD / 16;
+  // fp32 rows of 128: a lane's dimensions in four quarters of a row, so that a load of 16
+  // bytes a lane takes whole sectors (8 x 2000 rows of 4 heads, 8-bit: 21.5 us against
+  // 23.9); rows of 64 lose by it, their stores then being of half sectors or of more
+  // pieces (16 x up to 1000 rows of 8 heads, bf16: 20.4 against 17.9)
+  constexpr bool kQuarters = sizeof(TIn) == 4 && HD == 128;
+  constexpr int kAt = kQuarters ? 4 : 8, kSecond = kQuarters ? HD / 4 : 4;
   const int lane = threadIdx.x % kLanes, hkv = a.kv.n_kv_heads;
   const int group = blockIdx.x * (kAppendThreads / kLanes) + threadIdx.x / kLanes;
   const int t = group / a.spread, h0 = group - t * a.spread;
@@ -262,8 +280,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_cons
     const long long p = static_cast<long long>(a.positions[b]) + t;
     // this group's next rows to load; read before their place is known
     const long long k_step = a.ks.head * a.spread, v_step = a.vs.head * a.spread;
-    const TIn *k = static_cast<const TIn *>(a.k) + b * a.ks.seq + t * a.ks.token + h0 * a.ks.head + 8 * lane;
-    const TIn *v = static_cast<const TIn *>(a.v) + b * a.vs.seq + t * a.vs.token + h0 * a.vs.head + 8 * lane;
+    const TIn *k = static_cast<const TIn *>(a.k) + b * a.ks.seq + t * a.ks.token + h0 * a.ks.head + kAt * lane;
+    const TIn *v = static_cast<const TIn *>(a.v) + b * a.vs.seq + t * a.vs.token + h0 * a.vs.head + kAt * lane;
     const bool has_row = on;
     using Raw = Eight<TIn>[2][2];  // key and value, lower and upper half
     auto load = [&](Raw &raw, int h) {
@@ -272,8 +290,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_cons
         raw[0][half].clear();
         raw[1][half].clear();
         if (has_row && h < hkv) {
-          raw[0][half].load(k + half * (HD / 2), a.vec);
-          raw[1][half].load(v + half * (HD / 2), a.vec);
+          raw[0][half].load(k + half * (HD / 2), kSecond, a.vec);
+          raw[1][half].load(v + half * (HD / 2), kSecond, a.vec);
         }
       }
       k += k_step;
@@ -286,10 +304,11 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_cons
     // (cos, cos) and (sin, sin) of this lane's pairs of dimensions i, i + HD / 2
     float2 cos2[4], sin2[4];
     if (a.rope) {
-      const float2 *src = a.rope + (on && p >= 0 ? p * (HD / 2) : 0) + 8 * lane;
+      const float2 *src = a.rope + (on && p >= 0 ? p * (HD / 2) : 0) + kAt * lane;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 u = src[2 * i], w = src[2 * i + 1];
+        const int at = i < 2 ? 2 * i : kSecond + 2 * i - 4;
+        const float2 u = src[at], w = src[at + 1];
         cos2[i] = make_float2(u.x, w.x);
         sin2[i] = make_float2(u.y, w.y);
       }
@@ -299,8 +318,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_cons
     constexpr int kBytes = E4M3 ? 1 : 2;
     long long row = first + static_cast<long long>(h0) * a.kv.page_size;
     const long long row_step = static_cast<long long>(a.spread) * a.kv.page_size;
-    char *kd = static_cast<char *>(a.kv.k) + (row * HD + 8 * lane) * kBytes;
-    char *vd = static_cast<char *>(a.kv.v) + (row * HD + 8 * lane) * kBytes;
+    char *kd = static_cast<char *>(a.kv.k) + (row * HD + kAt * lane) * kBytes;
+    char *vd = static_cast<char *>(a.kv.v) + (row * HD + kAt * lane) * kBytes;
     for (int hb = 0; hb < hkv; hb += a.spread) {  // as often in every lane
       const int h = hb + h0;
       const bool put = on && h < hkv;
@@ -317,10 +336,10 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_cons
           x[j + 4] = fma2(lo, sin2[j], mul2(hi, cos2[j]));
         }
       }
-      put_row<HD, E4M3>(kd, a.kv.k_scale + row, put, x, lane);
+      put_row<HD, E4M3, kSecond>(kd, a.kv.k_scale + row, put, x, lane);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = vr[j / 4].pair(j % 4);
-      put_row<HD, E4M3>(vd, a.kv.v_scale + row, put, x, lane);
+      put_row<HD, E4M3, kSecond>(vd, a.kv.v_scale + row, put, x, lane);
       row += row_step;
       kd += row_step * (HD * kBytes);
       vd += row_step * (HD * kBytes);
