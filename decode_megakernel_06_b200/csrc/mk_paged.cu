@@ -460,9 +460,11 @@ __global__ void __launch_bounds__(kRowThreads) kv_gather(const __grid_constant__
 // Exactness.  bf16 rows are exact operands, and so are codes in fp16.  With a bf16
 // cache a query value and a weight enter as 3 truncated bf16 pieces, which are the
 // fp32 value itself; with bf16 rows in and out as two (2^-17 of it), well under the
-// output's rounding of 2^-8.  With codes they enter as 2 fp16 pieces, 2^-24 of the
-// value: queries of the row divided by a power of two, weights times their value's
-// scale under a reference that keeps them below 2^14.  Everything else is fp32.
+// output's rounding of 2^-8.  With codes they enter as 2 fp16 pieces, 2^-23 of the
+// value or half of fp16's smallest step: queries of the row multiplied by a power of two
+// that takes its largest to 2^10 or more, weights times their value's scale under a
+// reference that takes the row's largest to 2^6 and keeps it below 2^14.  Everything else is
+// fp32; what the tensor cores add, with truncation, is one unit's at most.
 // ---------------------------------------------------------------------------
 constexpr int kUnit = 16;          // positions per unit
 // A score may pass its row's reference by 2^kLazy before the reference is moved (fewer
@@ -1173,23 +1175,17 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           a2 = __byte_perm(vw[2][t], vw[3][t], 0x5410);
           a3 = __byte_perm(vw[2][t], vw[3][t], 0x7632);
         }
-        if constexpr (sizeof(TIO) == 4) {
-          // The tensor cores' fp32 sums truncate: kept in them over a long cache they fell
-          // behind by 7e-6 of the output (128k positions).  So each unit's is its own, and
-          // added with rounding.
+        // The tensor cores' fp32 sums truncate: kept in them over a long cache they fell
+        // behind by 8e-8 of the output a unit (7e-6 where 128k positions are split over the
+        // GPU, 1.3e-3 over a warp's share of a million).  So each unit's is its own, and added
+        // with rounding; 0 to 4% of the time where rows are bf16.
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NT; ++n) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = NP - 1; k >= 0; --k) mma<E4M3>(d, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+          for (int k = NP - 1; k >= 0; --k) mma<E4M3>(d, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[t][n][j] += d[j];
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma<E4M3>(acc[t][n], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+          for (int j = 0; j < 4; ++j) acc[t][n][j] += d[j];
         }
       }
       load_v(next);  // in flight through the next first product

@@ -416,9 +416,13 @@ MK_API uint64_t mk_paged_attention_workspace(void);
  *   out        : device [B][T][n_q_heads][head_dim] of `dtype`, contiguous, 16-byte
  *                aligned
  *   workspace  : see mk_paged_attention_workspace; 16-byte aligned
- * Scores, softmax statistics and sums are fp32.  The result does not depend on
- * which block finishes first.  One launch; asynchronous.  Errors: MK_ERR_ARG,
- * MK_ERR_UNSUPPORTED, MK_ERR_CAPACITY (workspace too small), MK_ERR_CUDA. */
+ * Scores, softmax statistics and sums are fp32.  The products take keys and values as
+ * held; q (rotated) and the weights enter them in fp32 over an MK_BF16 cache with
+ * MK_F32 rows, to 2^-17 of each with MK_BF16 rows (2^-8 is the output's rounding),
+ * and over an MK_E4M3 cache to 2^-23 of each or 2^-31 of its row's largest.
+ * The result does not depend on which block finishes first.  One launch;
+ * asynchronous.  Errors: MK_ERR_ARG, MK_ERR_UNSUPPORTED, MK_ERR_CAPACITY (workspace
+ * too small), MK_ERR_CUDA. */
 MK_API int mk_paged_attention(const mk_paged_kv *kv, const void *q, mk_strides qs, int32_t dtype, int32_t n_q_heads,
                               const int32_t *positions, const int32_t *counts, int32_t B, int32_t T, float scale,
                               const float *rope, int32_t rope_len, void *out, void *workspace,

@@ -240,6 +240,40 @@ def test_attention_long_sums_do_not_drift(kind):
         assert float((out[0, 0, 4 * h:4 * h + 4].double() - ref).norm() / ref.norm()) <= 16 * U
 
 
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("act", [F32, BF16], ids=["f32", "abf16"])
+def test_long_sums_keep_no_bias(kind, act):
+    """A million positions (64 pages, again and again: the softmax is that over one round of them),
+    with as many items as blocks, so that one warp adds 16384 units.  An error that always
+    points towards zero grows with their number; errors of single roundings do not.  The
+    mean relative error over N outputs in [1, 2): the outputs' own rounding, uniform
+    within half a step h of at most 2^-8 (bf16), has a standard deviation of h / sqrt(3 N),
+    of which 8 are allowed; and 64 u for the roundings of weights and sums."""
+    B, hkv, hq, hd, page, pages, rounds = 60, 8, 32, 64, 64, 64, 256
+    n = pages * page * rounds
+    g = torch.Generator(device=DEV).manual_seed(41)
+    k = torch.randn((pages, hkv, page, hd), generator=g, device=DEV)
+    v = 1 + torch.rand((pages, hkv, page, hd), generator=g, device=DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(rounds).expand(B, -1).contiguous()
+    if kind == BF16:
+        kv = mk.PagedKV(k.to(BF16), v.to(BF16), table)
+        kk, vv = kv.k.double(), kv.v.double()
+    else:
+        sk, sv = k.abs().amax(-1) / 448, v.abs().amax(-1) / 448
+        kv = mk.PagedKV((k / sk[..., None]).to(E4M3), (v / sv[..., None]).to(E4M3), table, sk, sv)
+        kk, vv = kv.k.double() * sk.double()[..., None], kv.v.double() * sv.double()[..., None]
+    q = (2 * torch.randn((B, 1, hq, hd), generator=g, device=DEV)).to(act)
+    out = torch.empty_like(q)
+    pos = torch.full((B,), n - 1, dtype=torch.int32, device=DEV)
+    assert kv.attention(q, pos, out, mk.paged_attention_workspace(q.device)) == mk.MK_OK
+    kk, vv = (x.transpose(0, 1).reshape(hkv, pages * page, hd) for x in (kk, vv))
+    qq = q[:, 0].double().reshape(B, hkv, hq // hkv, hd)
+    ref = torch.softmax(qq @ kk.transpose(-1, -2) * hd ** -0.5, -1) @ vv
+    err = (out[:, 0].double().reshape(ref.shape) - ref) / ref
+    h = torch.finfo(act).eps / 2
+    assert abs(float(err.mean())) <= 8 * h / math.sqrt(3 * err.numel()) + 64 * U
+
+
 def test_attention_many_sequences():
     lens = [1 + (37 * i) % 90 for i in range(700)]
     c = Cache(lens, 2, 64, 16, BF16, seed=6)
