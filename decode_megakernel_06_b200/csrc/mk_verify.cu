@@ -125,7 +125,10 @@ struct alignas(16) RowsShared {  // the queue and the cache behind it are read 1
   u64 fine[1 << kFine];       // read by the cluster
   u64 red[kVWarps], red2[kVWarps];
   uint32_t wkey[kVWarps], wkey2[kVWarps];
-  u64 cta_sum, cta_sum2;  // read by the cluster
+  // Read by the cluster, each written again only behind a cluster barrier: the first sum has a
+  // word of its own, since no barrier stands between its reading and the search's sums
+  // where no histogram is taken (top_p >= 1).
+  u64 cta_total, cta_sum, cta_sum2;
   float cta_least;
   uint32_t cta_key, cta_lo, cta_hi, n_cand;
   int32_t cta_id;
@@ -310,12 +313,12 @@ __global__ void __launch_bounds__(kVThreads, 1) verify_rows(const __grid_constan
     sum = warp_sum(sh.red[lane]);
     const uint32_t k = __reduce_min_sync(0xffffffffu, sh.wkey[lane]);
     if (lane == 0) {
-      sh.cta_sum = sum;
+      sh.cta_total = sum;
       sh.cta_least = key_logit(k);
     }
   }
   sync_all();
-  const u64 total = cluster_total(cluster, &sh.cta_sum, size, lane);
+  const u64 total = cluster_total(cluster, &sh.cta_total, size, lane);
   least = lane < (int)size ? *cluster.map_shared_rank(&sh.cta_least, lane) : INFINITY;
   least = key_logit(__reduce_min_sync(0xffffffffu, logit_key(least)));
   const u64 smallest = least < INFINITY ? mass_of(least, m, a.inv_t) : ~0ull;

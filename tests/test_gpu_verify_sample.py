@@ -16,6 +16,7 @@ import torch
 
 import decode_megakernel_06_b200 as mk
 from oracle import verify as overify
+from oracle.sample import masses, nucleus_need
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -275,3 +276,54 @@ def test_tensor_refusals():
     assert mk.verify_sample(lg, tok, 1.0, 1.0, None, out, acc, ws) == mk.MK_ERR_ARG
     assert mk.verify_sample(lg, tok, 1.0, 1.0, u, out, acc, ws[:16]) == mk.MK_ERR_CAPACITY
     assert mk.verify_sample(lg, tok, 1.0, 1.0, u, tok, acc, ws) == mk.MK_ERR_ARG
+
+
+def flat_row(V, tops, seed):
+    """`tops` tokens at one largest logit, the others 26 to 32.6 below it: masses of 0 to 360
+    units beside a sum above 2^53, of which fp64 keeps no single units.  The tail's ids, by
+    falling logit."""
+    rng = np.random.default_rng(seed)
+    row = np.full(V, 5.0, np.float32)
+    tail = rng.permutation(V)[:V - tops]
+    row[tail] = (5.0 - rng.uniform(26.0, 32.6, V - tops)).astype(np.float32)
+    return row, tail[np.argsort(-row[tail].astype(np.float64), kind="stable")]
+
+
+# Blocks few enough for clusters of 8, for clusters of 2 and for single CTAs.
+@pytest.mark.parametrize("V,tops,B", [(64000, 60000, 3), (64000, 400, 3), (131072, 131000, 2), (64000, 60000, 20),
+                                      (40001, 39000, 3), (9000, 8500, 90)])
+@pytest.mark.parametrize("certain", [True, False])
+def test_whole_distribution_whose_sum_is_rounded(V, tops, B, certain):
+    """top_p = 1 with need = ceil(fp64(Q)) below Q: the least tokens are left out, so the
+    nucleus is searched for although the whole distribution was asked for.  u = 0 keeps a
+    draft exactly if it belongs to the nucleus; drafts are those on both sides of its end."""
+    rows, drafts, left_out = [], [], 0
+    seed = 0
+    while len(rows) < B:
+        row, tail = flat_row(V, tops, seed)
+        seed += 1
+        a, q = overify.nucleus_masses(row, 1.0, 1.0), masses(row, 1.0).astype(np.int64)
+        total, lost = int(q.sum()), int(((q > 0) & (a == 0)).sum())
+        if nucleus_need(total, 1.0) >= total or not lost:
+            continue
+        end = int((a[tail] > 0).sum())  # tail[end - 1] is the last of the nucleus
+        at = (end - 1, end, end - 2, end + lost - 1, 0, len(tail) - 1)[len(rows) % 6]
+        rows.append(row)
+        drafts.append(int(tail[at]))
+        left_out += a[tail[at]] == 0
+    assert 0 < left_out < B
+    lg = np.stack([np.stack([r, rows[i - 1]]) for i, r in enumerate(rows)])
+    tok = np.array([[0, x] for x in drafts], np.int32)
+    u = np.stack([np.zeros(B), np.random.default_rng(V + B).random(B)], 1)
+    dr = None if certain else np.stack([r[None] for r in rows[1:] + rows[:1]])
+    out, acc = gpu(lg, dr, tok, 1.0, 1.0, u)
+    drawn = 0
+    for b in range(B):
+        ref = overify.verify_block(lg[b], None if certain else dr[b], tok[b], 1.0, 1.0, u[b])
+        assert acc[b] == ref.accepted, b
+        if ref.draw_margin >= 8 * V:
+            assert out[b].tolist() == ref.tokens, b
+            drawn += 1
+    assert drawn >= B // 2
+    again = gpu(lg, dr, tok, 1.0, 1.0, u)
+    assert (again[0] == out).all() and (again[1] == acc).all()
