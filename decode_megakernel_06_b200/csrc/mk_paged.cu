@@ -211,14 +211,26 @@ __device__ __forceinline__ void put_row(char *dst, float *scale_at, bool on, flo
         x[i].y = fabsf(x[i].y) == INFINITY ? copysignf(most, x[i].y) : x[i].y;
       }
     }
-    // Quotients a / b, correctly rounded: y = a r with r = 1 / b, and its remainder once
-    // more, y + r (a - y b) (Markstein, Computation of elementary functions on the IBM
-    // RISC System/6000 processor, 1990).
+    // Quotients a / b: y = a r with r = 1 / b, and its remainder once more, y + r (a - y b)
+    // (Markstein, Computation of elementary functions on the IBM RISC System/6000
+    // processor, 1990).  For scales of 2^-80 up and the values next to e4m3's midpoints that is
+    // the correctly rounded quotient for every mantissa of the scale; below, remainders
+    // leave fp32's range, so such a row is first multiplied by a power of two, as its
+    // scale is.
     constexpr float k448 = 1.0f / kE4m3Max;
     const float s0 = amax * k448;
     const float scale = fmaxf(fmaf(fmaf(-s0, kE4m3Max, amax), k448, s0), kTinyScale);
-    const float r = __frcp_rn(scale);
-    const float2 r2 = make_float2(r, r), s2 = make_float2(-scale, -scale);
+    float by = scale;
+    constexpr float kSmallRow = 8.2718061255e-25f, kUp = 1.2676506002e30f;  // 2^-80, 2^100
+    const bool small = amax > 0.f && amax < kSmallRow;
+    if (__any_sync(0xffffffffu, small)) {
+      const float up = small ? kUp : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(up, up));
+      by *= up;
+    }
+    const float r = __frcp_rn(by);
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-by, -by);
     float2 q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

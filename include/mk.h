@@ -370,8 +370,9 @@ typedef struct mk_strides {
  *                i with i + head_dim / 2), in fp32; a row at or past rope_len is not written
  *   MK_BF16    : each value is rounded to nearest even.
  *   MK_E4M3    : per row of head_dim values x: scale = max(amax / 448, 2^-126),
- *                code = round-to-nearest-even(x / scale); amax is over the finite values,
- *                infinities become the largest code of their sign, NaN stays NaN.
+ *                code = round-to-nearest-even(x / scale), both quotients in fp32, correctly
+ *                rounded; amax is over the finite values, infinities become the largest
+ *                code of their sign, NaN stays NaN.
  * Rows at negative positions, past the table's end or on unmapped pages are not
  * written; rows that two sequences map to one slot are the caller's race.
  * Needs no workspace; one launch; asynchronous on `stream`.  Errors: MK_ERR_ARG,

@@ -534,6 +534,45 @@ def test_append_special_values():
     assert torch.equal(c.kv.k_scale.cpu()[pg, 0], s) and torch.equal(c.kv.v_scale.cpu()[pg, 0], s)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("act", [F32, BF16], ids=["f32", "abf16"])
+def test_append_midpoints_at_every_scale(hd, act):
+    """Values at and next to the midpoints between codes, with scales from 2^-126 to 2^110
+    of random mantissas: exactly the codes of the fp32 quotients x / scale (compared as the
+    values they stand for: a zero may have either sign)."""
+    g = gen(32)
+    T, B = 237 * 4, 3
+    e = (torch.arange(T) // 4 - 126).double()
+    s = torch.exp2(e) * (1 + torch.rand((B, T), generator=g, dtype=torch.float64))
+    amax = (448 * s).float().to(act).float()
+    s = (amax / 448).clamp_min(2.0 ** -126).double()
+    mid = torch.cat([(torch.arange(16, 32) + 0.5) / 16 * 2.0 ** i for i in range(-6, 8)])
+    mid = torch.cat([mid, (torch.arange(16) + 0.5) * 2.0 ** -9])
+    mid = mid[mid < 440]
+    pick = mid[torch.randint(len(mid), (B, T, hd), generator=g)] * torch.where(torch.rand((B, T, hd), generator=g) < 0.5, -1, 1)
+    x = (pick * s[..., None]).float()
+    step = torch.randint(-2, 3, x.shape, generator=g)
+    for _ in range(2):
+        x = torch.where(step > 0, torch.nextafter(x, torch.full_like(x, 1e38)), x)
+        x = torch.where(step < 0, torch.nextafter(x, torch.full_like(x, -1e38)), x)
+        step = step - step.sign()
+    x = x.to(act).float()
+    x[..., 5] = amax
+    codes, scales = expected_codes(x)
+    c = Cache([T] * B, 1, hd, 64, E4M3, seed=33)
+    c.cuda()
+    xg = x[:, :, None].to(act).to(DEV)
+    assert c.kv.append(xg, -xg, torch.zeros(B, dtype=torch.int32, device=DEV)) == mk.MK_OK
+    minus = expected_codes(-x)[0]
+    got_k, got_v, got_s = c.kv.k.cpu().float(), c.kv.v.cpu().float(), c.kv.k_scale.cpu()
+    for b in range(B):
+        where = [c.at(b, t) for t in range(T)]
+        pg, slot = (torch.tensor([w[i] for w in where]) for i in (0, 1))
+        assert torch.equal(got_s[pg, 0, slot], scales[b])
+        assert torch.equal(got_k[pg, 0, slot], codes[b].float())
+        assert torch.equal(got_v[pg, 0, slot], minus[b].float())
+
+
 def test_append_outside_the_cache():
     """Negative positions, rows past the table and past rope are dropped."""
     c = Cache([16, 16, 16], 2, 64, 8, BF16, seed=25)
