@@ -1090,13 +1090,18 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[n][j] *= E4M3 ? f[n][j & 1] * ks_[j >> 1] : f[n][j & 1];
+      // -inf is a masked score; one that is not masked comes of what is not finite, or lies outside
+      // of fp32's range, and makes its row NaN
+      const float none = full ? NAN : 0.f;  // the weight of -inf
       if (!full) {
         const int rj[2] = {__shfl_sync(0xffffffffu, row, g), __shfl_sync(0xffffffffu, row, g + 8)};
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
+            if (s[n][j] == -INFINITY) s[n][j] = NAN;
             if (rj[j >> 1] < 0 || p0 + g + 8 * (j >> 1) > s_lim[8 * n + 2 * c + (j & 1)]) s[n][j] = -INFINITY;
+          }
       }
       // the rows' references, moved where a score passes one by more than kLazy
       bool over = false;
@@ -1131,7 +1136,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float x = s[n][j];
-          const float w = x == -INFINITY ? 0.f : ex2(x - m[n][j & 1]);
+          const float w = x == -INFINITY ? none : ex2(x - m[n][j & 1]);
           l[n][j & 1] += w;
           s[n][j] = !E4M3 || x == -INFINITY ? w : w * vs_[j >> 1];
         }

@@ -404,7 +404,8 @@ MK_API uint64_t mk_paged_attention_workspace(void);
  * over the mapped positions.  A row that sees no position gives zeros.  Values
  * behind a row's last position, and on unmapped pages, are never used, whatever
  * they hold.  A key, value or scale that is not finite makes the outputs of the rows
- * that see it not finite (a value: in its dimension).
+ * that see it not finite (a value: in its dimension), and so does a score outside of
+ * fp32's range in its row.
  *   q          : device [B][T][n_q_heads][head_dim] of `dtype` (MK_F32 or MK_BF16),
  *                strides `qs`
  *   positions  : device int32 [B]: position of row 0; negative: rows at negative

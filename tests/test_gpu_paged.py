@@ -100,6 +100,13 @@ class Cache:
         return k, v, held
 
 
+def again(c):
+    """A Cache of the same pages, to be uploaded anew."""
+    d = object.__new__(Cache)
+    d.__dict__.update({k: v for k, v in c.__dict__.items() if k != "kv"})
+    return d
+
+
 def turned(x, rope, p):
     """Rotate-half of x [..., hd] in 64 bits by the table's entry for p."""
     half = x.shape[-1] // 2
@@ -336,6 +343,57 @@ def test_attention_ignores_what_is_masked(kind, bad):
     assert not torch.isfinite(got[1, 3:]).any()
     assert torch.isnan(got[2, 4, :2, 3]).all() and torch.isfinite(got[2, 4, :2, :3]).all()  # v: its dimension alone
     assert torch.isnan(got[2, 4, 2:]).all()  # k: the whole row
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("act", [F32, BF16], ids=["f32", "abf16"])
+@pytest.mark.parametrize("at", [3, 61, 130])
+def test_attention_scores_of_minus_infinity(kind, act, at):
+    """A key (or its scale) that is not finite and scores -inf: the rows that see it are
+    not finite, wherever it stands; rows before it and the other head are right."""
+    T, n = 5, 133
+    c = Cache([n, n], 2, 64, 16, kind, seed=34)
+    pg, slot = c.at(0, at)
+    if kind == BF16:
+        c.k[pg, 0, slot, 9] = -float("inf")
+    else:
+        c.k[pg, 0, slot] = (-c.k[pg, 0, slot].float().abs() - 1).to(E4M3)
+        c.ks[pg, 0, slot] = float("inf")
+    q = (torch.rand((2, T, 4, 64), generator=gen(35)) + 0.5).to(act)
+    out = torch.full(q.shape, 7.0, dtype=act, device=DEV)
+    c.cuda()
+    pos = [n - T, n - T]
+    ws = mk.paged_attention_workspace(torch.device(DEV))
+    assert c.kv.attention(q.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV), out, ws) == mk.MK_OK
+    got = out.cpu().float()
+    sees = torch.arange(n - T, n) >= at
+    assert not torch.isfinite(got[0, sees, :2]).any() and torch.isfinite(got[0, ~sees, :2]).all()
+    assert torch.isfinite(got[0, :, 2:]).all() and torch.isfinite(got[1]).all()
+    if kind == BF16:
+        c.k[pg, 0, slot, 9] = 0
+    else:
+        c.ks[pg, 0, slot] = 1.0
+    good = check_attention(again(c), q, pos).cpu()
+    got = out.cpu()
+    got[0, sees, :2] = good[0, sees, :2]
+    compare_attention(c, q, pos, None, None, None, got)
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_attention_scores_beyond_fp32(kind):
+    """Rows whose every score is -inf see positions all the same: NaN, not the zeros of a row
+    that sees none."""
+    c = Cache([70], 1, 64, 16, kind, seed=36)
+    c.k = c.k.float().abs().clamp_min(0.25).to(kind)
+    q = torch.ones((1, 2, 4, 64))
+    q[0, :, 1, 3] = -float("inf")
+    q[0, :, 2] = -1e38
+    out = torch.full(q.shape, 7.0, device=DEV)
+    ws = mk.paged_attention_workspace(torch.device(DEV))
+    pos = torch.tensor([68], dtype=torch.int32, device=DEV)
+    assert c.cuda().attention(q.to(DEV), pos, out, ws, scale=100.0) == mk.MK_OK
+    got = out.cpu()
+    assert torch.isnan(got[0, :, 1:3]).all() and torch.isfinite(got[0, :, ::3]).all()
 
 
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
