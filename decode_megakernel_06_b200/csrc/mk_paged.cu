@@ -488,6 +488,7 @@ struct Lazy {
   static constexpr float kLazy = E4M3 ? 14.0f : 8.0f, kBase = E4M3 ? 6.0f : 0.0f;
 };
 constexpr float kLeastScale = -80.0f;  // log2 of scales below it counts as this: the sums of weights stay finite
+constexpr float kLeastValueScale = 8.2718061255e-25f;  // 2^kLeastScale
 constexpr int kMinUnits = 8;       // units per block, at least
 constexpr int kSecondItem = 32;    // what a second item costs a block, in units
 constexpr int kJoinBits = 3;       // parts of an item that one block joins, all their loads in flight; more are
@@ -815,6 +816,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
   __shared__ int s_lim[kRows];                  // last position a row sees, -1: none
   __shared__ float s_m[kAtWarps][kRows], s_l[kAtWarps][kRows];
   __shared__ float s_M[kRows], s_L[kRows];
+  __shared__ float s_down[E4M3 ? kAtWarps : 1][kRows];  // of a unit with tiny value scales
   __shared__ long long s_out[kRows];            // first element of a row of the output, -1: no such row
   __shared__ uint32_t s_last;
   __shared__ int s_bad;
@@ -1073,6 +1075,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           for (int i = NQ - 2; i >= 0; --i) s[n][j] += sp[i][n][j];
         }
       float ks_[2] = {1.f, 1.f}, vs_[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+      const bool small = E4M3 && vsc != 0.f && fabsf(vsc) < kLeastValueScale;
       if constexpr (E4M3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -1084,8 +1087,7 @@ paged_attn(const __grid_constant__ AttnArgs p) {
       load_k(next);  // in flight through the softmax and the second product
 
       // scores (element j: position g + 8 (j / 2), row 2 c + j % 2 of tile n); masks
-      const bool held = __all_sync(0xffffffffu, row >= 0);
-      const bool full = held && p0 + kUnit - 1 <= all_see;
+      const bool full = __all_sync(0xffffffffu, row >= 0 && !small) && p0 + kUnit - 1 <= all_see;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1140,6 +1142,32 @@ paged_attn(const __grid_constant__ AttnArgs p) {
           l[n][j & 1] += w;
           s[n][j] = !E4M3 || x == -INFINITY ? w : w * vs_[j >> 1];
         }
+      // Value scales too small for the reference's clamp: a row's products, and its sums so far,
+      // are multiplied by a power of two that takes the unit's largest to 2^6, for the
+      // time of the product.  2^46 is what the clamp takes at most; sums stay below 2^54.
+      const bool tiny = E4M3 && !full && __any_sync(0xffffffffu, small);
+      if (tiny) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = fmaxf(fabsf(s[n][j]), fabsf(s[n][j + 2]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const int bits = x > 0.f ? min(max(6 + 127 - static_cast<int>(__float_as_uint(x) >> 23), 0), 46) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
+            s[n][j] *= up;
+            s[n][j + 2] *= up;
+#pragma unroll
+            for (int t = 0; t < KS; ++t) {
+              acc[t][n][j] *= up;
+              acc[t][n][j + 2] *= up;
+            }
+            if (g == 0) s_down[warp][8 * n + 2 * c + j] = __uint_as_float(static_cast<uint32_t>(127 - bits) << 23);
+          }
+        __syncwarp();
+      }
       if (!full) {
         // V values that only some rows see meet the others' zero weights: one that is not
         // finite is taken out here, and put into the rows that see it below.
@@ -1206,6 +1234,16 @@ paged_attn(const __grid_constant__ AttnArgs p) {
         }
       }
       load_v(next);  // in flight through the next first product
+      if (tiny) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float down = s_down[warp][8 * n + 2 * c + (j & 1)];
+#pragma unroll
+            for (int t = 0; t < KS; ++t) acc[t][n][j] *= down;
+          }
+      }
       row = next;
       next = after;
     }

@@ -435,6 +435,26 @@ def test_attention_values_of_very_different_size():
     assert float((out[0, 0].cpu().double() - ref).abs().max()) <= (4 * ds + 150 * U) * rest
 
 
+@pytest.mark.parametrize("exp", [-70, -84, -100, -113, -126])
+@pytest.mark.parametrize("act", [F32, BF16], ids=["f32", "abf16"])
+def test_attention_tiny_value_scales(exp, act):
+    """Value scales down to 2^-126, the least that an append gives, to the same relative bound;
+    beside far smaller ones, rows of zeros, and a large one that only the last row sees."""
+    T = 4
+    lens = [33, 150, 90, 64]
+    c = Cache(lens, 2, 64, 16, E4M3, seed=37)
+    c.vs = torch.exp2(torch.full_like(c.vs, exp))
+    for p in range(0, 90, 3):
+        pg, slot = c.at(2, p)
+        c.vs[pg, :, slot] = 2.0 ** max(exp - 20, -126)
+        pg, slot = c.at(2, p + 1)
+        c.v[pg, :, slot], c.vs[pg, :, slot] = 0, 2.0 ** -126
+    pg, slot = c.at(3, 63)
+    c.vs[pg, :, slot] = 1.0
+    q = torch.randn((4, T, 10, 64), generator=gen(38)).to(act)
+    check_attention(c, q, [n - T for n in lens], rope=rope_table(160, 64))
+
+
 def test_attention_operand_layouts():
     """q as a slice of a fused row, then at an odd offset (no 16-byte loads)."""
     lens = [70, 90]
