@@ -13,7 +13,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 #include <utility>
 
 #include "mk_internal.h"
@@ -1449,10 +1448,11 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
 }
 
 // Groups per token and the grid: heads of a token are spread over groups while
-// there are too few tokens to fill the GPU (about 64 groups of an SM).
+// there are too few tokens to fill a B200's SMs (about 64 groups each).
+constexpr int kSms = 148;
 dim3 row_grid(const mk_paged_kv &kv, int threads, int lanes, int B, int T, int &spread) {
   const int per = threads / lanes;
-  const long long tokens = static_cast<long long>(B) * T, want = 148 * 64;
+  const long long tokens = static_cast<long long>(B) * T, want = kSms * 64;
   spread = static_cast<int>(std::max(1ll, std::min<long long>(kv.n_kv_heads, want / tokens)));
   const unsigned groups = static_cast<unsigned>(T) * spread;  // checked to fit by the caller
   return dim3((groups + per - 1) / per, std::min(B, 65535));
@@ -1505,6 +1505,7 @@ template <int HD, typename TIO, bool E4M3, int NT>
 static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStream_t st) {
   using S = AtShape<HD, TIO, E4M3, NT>;
   static_assert(S::kBlocks * S::kRows <= 48 && HD <= 128, "workspace");
+  static_assert(S::kSmem <= 40 * 1024, "no opt-in needed beside the static shared memory");
   const int blocks = std::min(n_sm * S::kBlocks, kAtMaxBlocks);
   p.n_rg = (p.R + S::kRows - 1) / S::kRows;
   p.few = p.a.B <= 32 && p.n_rg <= 8 &&
@@ -1512,17 +1513,6 @@ static cudaError_t run_attention(AttnArgs &p, void *workspace, int n_sm, cudaStr
   p.count = static_cast<uint32_t *>(workspace);
   p.part = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + kCountBytes);
   p.part_ml = reinterpret_cast<float2 *>(p.part + static_cast<size_t>(2) * blocks * S::kRows * HD / 4);
-  if (S::kSmem > 40 * 1024) {
-    static std::atomic<uint64_t> done{0};  // devices on which the size is set
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
-      e = cudaFuncSetAttribute(paged_attn<HD, TIO, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
-    }
-  }
   return launch(paged_attn<HD, TIO, E4M3, NT>, dim3(blocks), dim3(S::kThreads), S::kSmem, st, p);
 }
 
