@@ -289,6 +289,16 @@ def test_attention_many_sequences():
 
 
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lo,hi", [(700, 2600), (1500, 1500)])
+def test_attention_equal_parts_of_many_sequences(kind, lo, hi):
+    """More than 32 sequences, each long enough to be cut into several parts of one size."""
+    lens = [lo + (hi - lo) * ((29 * i) % 37) // 36 for i in range(37)]
+    c = Cache(lens, 1, 64, 48, kind, seed=39)
+    q = torch.randn((37, 2, 3, 64), generator=gen(40))
+    check_attention(c, q, [n - 2 for n in lens], counts=[2 - (i % 5 == 4) for i in range(37)])
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
 def test_attention_rows_that_see_nothing(kind):
     lens = [40, 40, 40, 40, 40]
     c = Cache(lens, 2, 64, 16, kind, seed=7)

@@ -7,6 +7,8 @@ holds as bf16 pairs (2^-17 of a value, a few of them in each of the tiny model's
 layers), and in the order of its sums.  1e-3 of the largest logit leaves room for
 that through the layers; a wrong position, head or page is far outside.
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -196,3 +198,60 @@ def test_refusals(weights):
     one = mk.Decoder(TINY, weights, max_rows=1, max_seqs=1, kv_capacity=64)
     assert one.step_paged(tok, pos, 1, 1, pages.layers, None, am) == mk.MK_ERR_UNSUPPORTED
     one.close()
+
+
+WIDE_HEADS = dataclasses.replace(TINY, name="tiny_128", head_dim=128)
+
+
+def two_ways(model, weights, kind, B, T, lens, page, cap=192, steps=2):
+    """The logits of a few steps over pages of `kind`, and over a contiguous bf16 cache that holds
+    the same values: 8-bit pages have powers of two for scales, so that bf16 holds code * scale."""
+    L, H, hd = model.n_layers, model.n_kv_heads, model.head_dim
+    g = torch.Generator(device=DEV).manual_seed(11)
+    width = -(-cap // page)
+    n = B * width + 2
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(2))[:B * width].reshape(B, width).to(torch.int32).to(DEV)
+    dec = mk.Decoder(model, weights, max_rows=max(2, B * T), max_seqs=B, kv_capacity=cap, variant="tensorcore")
+    k, v = (torch.zeros((L, B, H, cap, hd), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    layers = []
+    for l in range(L):
+        pools = [torch.randn((n, H, page, hd), generator=g, device=DEV) for _ in range(2)]
+        scales = [None, None]
+        if kind == torch.bfloat16:
+            pools = [x.to(kind) for x in pools]
+        else:
+            pools = [(100 * x).clamp(-448, 448).to(kind) for x in pools]
+            scales = [torch.exp2(torch.randint(-9, -4, (n, H, page), generator=g, device=DEV).float()) for _ in range(2)]
+        kv = mk.PagedKV(*pools, table, *scales)
+        views = [x[l][:, :, :max(lens)].transpose(1, 2) for x in (k, v)]
+        assert kv.gather(i32([0] * B), *views, counts=i32(lens)) == mk.MK_OK
+        layers.append(kv)
+    got, pos, tokens = [], list(lens), list(make_tokens(model.vocab, B * T, seed=5))
+    for _ in range(steps):
+        pair = []
+        for paged in (True, False):
+            logits = torch.full((B * T, model.vocab), float("nan"), device=DEV)
+            am = torch.full((B * T,), -1, dtype=torch.int32, device=DEV)
+            rc = (dec.step_paged(i32(tokens), i32(pos), B, T, layers, logits, am) if paged else
+                  dec.step(i32(tokens), i32(pos), B, T, k, v, logits, am))
+            assert rc == mk.MK_OK and dec.status() == mk.MK_OK, mk.mk_last_error()
+            pair.append(logits.cpu().numpy())
+        got.append(pair)
+        pos = [p + T for p in pos]
+    dec.close()
+    return got
+
+
+@pytest.mark.parametrize("model", [TINY, WIDE_HEADS], ids=["64", "128"])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float8_e4m3fn], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B,T,page", [(3, 2, 24), (9, 1, 16), (2, 7, 64)])
+def test_old_positions_count_as_in_the_contiguous_cache(model, kind, B, T, page):
+    """Both head sizes and both caches, the whole of the logits.  The key and value projections
+    are zero, so that the new rows are zeros, which either cache holds exactly, and the
+    steps differ in their attention's arithmetic alone."""
+    w = make_weights(model, 0, DEV)
+    for lw in w["layers"]:
+        lw["wqkv"][model.n_q_heads * model.head_dim:] = 0
+    lens = [127 - 11 * b for b in range(B)]
+    for paged, flat in two_ways(model, w, kind, B, T, lens, page):
+        assert relerr(paged, flat) <= TOL

@@ -327,3 +327,14 @@ def test_whole_distribution_whose_sum_is_rounded(V, tops, B, certain):
     assert drawn >= B // 2
     again = gpu(lg, dr, tok, 1.0, 1.0, u)
     assert (again[0] == out).all() and (again[1] == acc).all()
+
+
+@pytest.mark.parametrize("scale", [50.0, 1e-3, 0.0, 1e30])
+@pytest.mark.parametrize("temperature", [1.0, 3.0, 1e-30])
+@pytest.mark.parametrize("top_p", [1.0, 0.9])
+def test_peaked_and_flat_rows_are_compared(scale, temperature, top_p):
+    """Five blocks of six, at least, are clear of their borders, and are compared."""
+    lg, dr, tok, u = block(6, 4, 2000, 4)
+    lg, dr = (lg * np.float32(scale)).astype(np.float32), (dr * np.float32(scale)).astype(np.float32)
+    assert compare(lg, dr, tok, temperature, top_p, u) >= 5
+    assert compare(lg, None, tok, temperature, top_p, u) >= 5
