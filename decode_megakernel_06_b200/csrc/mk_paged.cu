@@ -131,7 +131,7 @@ struct Four<__nv_bfloat16> {
 // of x / scale with scale = max(amax / 448, 2^-126) over the row's finite values (half a
 // step of e4m3, 2^-4 relative; a true quotient keeps x = amax on the largest code).
 // Every lane of a warp stays in the shuffles; rows without a place are not written.  Each input byte is read once, each cache byte
-// written once: 30.4 us for 135 MB (4.4 TB/s), bound by the instructions of rounding
+// written once: 30.1 us for 135 MB (4.5 TB/s), bound by the instructions of rounding
 // and scaling beside the loads' latency.
 // ---------------------------------------------------------------------------
 constexpr int kHeadsAtOnce = 2;  // heads whose key and value rows a group of a gather loads together
@@ -269,16 +269,18 @@ __device__ __forceinline__ void put_row(char *dst, float *scale_at, bool on, flo
   }
 }
 
-// 5 blocks of 128 threads per SM: 20 warps cover more of the loads' latency than 16 (35.3 us for
-// 8 x up to 4096 rows into an 8-bit cache, 30.4 here); at 24 registers spill (35.3).
+// 5 blocks of 128 threads per SM: with bf16 rows 20 warps cover more of the loads' latency than 16
+// (8 x up to 4096 rows: 34.8 us into an 8-bit cache and 38.8 into bf16, 30.2 and 33.7 here);
+// at 24 registers spill (35.5 and 36.5).  fp32 rows spill at 20 already, 76 to 92 bytes,
+// and would be faster at 16 (8 x 2000 rows of 4 heads, 8-bit: 17.9 us against 22.0).
 template <int HD, typename TIn, bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads, 5) kv_append(const __grid_constant__ KvAppend a) {
   pdl_wait();
   pdl_launch();
   constexpr int kLanes = HD / 16;
   // fp32 rows of 128: a lane's dimensions in four quarters of a row, so that a load of 16
-  // bytes a lane takes whole sectors (8 x 2000 rows of 4 heads, 8-bit: 21.5 us against
-  // 23.9); rows of 64 lose by it, their stores then being of half sectors or of more
+  // bytes a lane takes whole sectors (8 x 2000 rows of 4 heads, 8-bit: 22.0 us against
+  // 24.5); rows of 64 lose by it, their stores then being of half sectors or of more
   // pieces (16 x up to 1000 rows of 8 heads, bf16: 20.4 against 17.9)
   constexpr bool kQuarters = sizeof(TIn) == 4 && HD == 128;
   constexpr int kAt = kQuarters ? 4 : 8, kSecond = kQuarters ? HD / 4 : 4;
@@ -452,11 +454,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_gather(const __grid_constant__
 // (a counter per group) joins theirs in the order of the blocks, then the last of
 // eight such groups, so that the result does not depend on who was last.
 //
-// Measured (B200, 6.56 TB/s copy): 4 caches of 131072, bf16, 32/8 heads of 128: 345 us,
-// 6.2 TB/s; 8 of 4096: 33 us, of which the loads take 20 and the rest is the counting,
+// Measured (B200, 6.56 TB/s copy): 4 caches of 131072, bf16, 32/8 heads of 128: 327 to 340 us,
+// 6.3 to 6.6 TB/s; 8 of 4096: 33 us, of which the loads take 20 and the rest is the counting,
 // the first pages' chain of loads, the merge and the join; 32 8-bit caches of 512 to 2048:
-// 20 us, 8 blocks of 7 rows at 2048: 27 us, bound by the warps' instructions (products,
-// conversions, exponentials) at 12 warps per SM.
+// 21 us, 8 blocks of 7 rows at 2048: 26 us.  Of these two the units take 9 and 12 us (products,
+// conversions, exponentials at 12 warps per SM), the chain before them 6 and 8, the merge,
+// the parts and the join after them 4 and 6.
 //
 // A unit is one warp's: S^T = K Q^T and O^T += V^T P^T on mma.sync, positions and
 // then head dimensions as M = 16, query rows as N = 8.  Decoding has few rows, so a
@@ -491,7 +494,7 @@ constexpr float kLeastValueScale = 8.2718061255e-25f;  // 2^kLeastScale
 constexpr int kMinUnits = 8;       // units per block, at least
 constexpr int kSecondItem = 32;    // what a second item costs a block, in units
 constexpr int kJoinBits = 3;       // parts of an item that one block joins, all their loads in flight; more are
-constexpr int kJoin = 1 << kJoinBits;  // joined in levels (one cache of 8192: 23.5 us by 32 at a time, 20.7 by 16, 18.5 by 8)
+constexpr int kJoin = 1 << kJoinBits;  // joined in levels (one cache of 8192: 51.2 us by 32 at a time, 25.1 by 16, 18.2 by 8)
 constexpr int kLevels = 3;
 constexpr int kAtMaxBlocks = kJoin * kJoin * kJoin;  // blocks of a grid, at most
 
@@ -655,8 +658,9 @@ __device__ __forceinline__ int weight_of(int n, int size) { return size == 1 ? n
 // (parts <= units / size + items <= blocks): no block pays for a second prologue, merge
 // and join, but the longest part (`longest`: the longest item) sets the time.  Parts
 // are taken while that is at most 5/4 of a share and a second item.  Measured, parts
-// against shares: 32 sequences of 512 to 2048 21.8 and 25.7 us; 8 x 4096 34.2 and 37.7;
-// 4 x 131072 330 and 348; 24 of 3000 to 12000 (192 items) 94 and 68.
+// against shares: 32 sequences of 512 to 2048 20.9 and 24.0 us; 8 x 4096 33.0 and 36.4;
+// one of 8192 18.2 and 21.7; 24 of 3000 to 12000 (192 items) 167 and 132; 4 x 131072,
+// where a prologue is little beside the loads, 340 and 333 (parts all the same).
 template <typename I>
 __device__ __forceinline__ int part_size(I units, I items, int longest, int grid) {
   if (items >= grid) return 1;

@@ -199,8 +199,10 @@ __device__ __forceinline__ void each(const float *src, int n, int vec4, int tid,
 
 // One cluster per row (of one CTA where there are rows enough).  The row is read from
 // memory once and from L2 or shared memory after that: for the largest logit, for the
-// masses, and where a nucleus has to be found for its tokens.  The masses, an fp64
-// exponential per logit, bound this kernel.
+// masses, and where a nucleus has to be found for its tokens.  What bounds it with a nucleus
+// is one phase after another: of some 31 us for 104 rows of 32000 the masses, an fp64
+// exponential per logit, and their exact pass take 13, issue slots are 62% used and the
+// fp64 pipe 17%.  Of the whole distribution the masses are most.
 //
 // The nucleus: a token is left out if all tokens whose masses are no larger weigh no
 // more than Q - need, so one whose mass is below (Q - need) / V need not be counted.
